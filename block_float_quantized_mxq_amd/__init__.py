@@ -1,5 +1,6 @@
 """Python binding of libmxq: block-float (MXFP4 / MXFP8 / NVFP4) quantized GEMV,
-expert-indexed MoE GEMV and prefill GEMM on AMD MI355X (gfx950).
+expert-indexed MoE GEMV and prefill GEMM on AMD MI355X (gfx950), and what runs between
+a layer's QKV and output projections (kv.py: rotary positions, paged cache, attention).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of ``libmxq.so`` behind the C ABI in ``include/mxq.h``.  PyTorch
@@ -18,6 +19,10 @@ import ctypes
 import os
 
 import torch
+
+from . import kv as _kv
+from .kv import (KVCache, kv_append, kv_cache, paged_attn, paged_attn_workspace, rope,  # noqa: F401
+                 rope_inv_freq)
 
 MXFP4, MXFP8, NVFP4 = 1, 2, 3
 FORMATS = {"mxfp4": MXFP4, "mxfp8": MXFP8, "nvfp4": NVFP4}
@@ -71,6 +76,7 @@ def lib() -> ctypes.CDLL:
         L.mxq_status_string.argtypes = [I]
         L.mxq_status_string.restype = ctypes.c_char_p
         L.mxq_abi_version.restype = I
+        _kv.bind(L)
         _lib = L
     return _lib
 

@@ -8,32 +8,20 @@
 #include <cstring>
 
 #include "../../include/mxq.h"
+#include "api_util.hpp"
 #include "kernels.hpp"
 
-#define MXQ_API extern "C" __attribute__((visibility("default")))
-
 namespace {
-
-using mxq::kMXFP4;
-using mxq::kMXFP8;
-using mxq::kNVFP4;
-
-bool valid_fmt(int fmt) { return fmt == kMXFP4 || fmt == kMXFP8 || fmt == kNVFP4; }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
-// Prefill GEMMs with at most this many token rows run on the matrix-unit GEMV
-// (16 rows per launch).
-constexpr int64_t kSmallGemmRows = 32;
 
 // Per-device result of the gfx950 check: 0 unknown, 1 ok, 2 not usable; and
 // the device's compute-unit count.
 std::atomic<int> g_device_ok[64];
 std::atomic<int> g_device_cus[64];
 
+}  // namespace
+
 // gfx950 check of the current device; on success *cus is its compute-unit count.
-mxq_status_t check_device(int* cus) {
+mxq_status_t mxq::check_device(int* cus) {
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0) {
         (void)hipGetLastError();
@@ -56,6 +44,23 @@ mxq_status_t check_device(int* cus) {
     return MXQ_OK;
 }
 
+namespace {
+
+using mxq::aligned;
+using mxq::as_stream;
+using mxq::check_device;
+using mxq::launched;
+using mxq::kMXFP4;
+using mxq::kMXFP8;
+using mxq::kNVFP4;
+
+bool valid_fmt(int fmt) { return fmt == kMXFP4 || fmt == kMXFP8 || fmt == kNVFP4; }
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+// Prefill GEMMs with at most this many token rows run on the matrix-unit GEMV
+// (16 rows per launch).
+constexpr int64_t kSmallGemmRows = 32;
+
 mxq_status_t check_weight(int fmt, const uint8_t* codes, const uint8_t* scales, const float* gscale) {
     if (!valid_fmt(fmt)) return MXQ_E_FORMAT;
     if ((fmt == kNVFP4) != (gscale != nullptr)) return MXQ_E_FORMAT;
@@ -67,13 +72,6 @@ mxq_status_t check_k(int fmt, int64_t k) {
     if (k <= 0 || k % mxq::block_elems(fmt) != 0) return MXQ_E_SHAPE;
     return MXQ_OK;
 }
-
-mxq_status_t launched(bool ok) {
-    if (!ok) return MXQ_E_UNSUPPORTED;
-    return hipGetLastError() == hipSuccess ? MXQ_OK : MXQ_E_LAUNCH;
-}
-
-hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 }  // namespace
 
