@@ -14,6 +14,11 @@ using mxq::aligned;
 constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxTokens = int64_t(1) << 22;  // one workgroup a token: 2^30 work items
 
+constexpr int64_t kMaxRows = int64_t(1) << 25;      // query rows: workgroups of every launch stay below 2^24
+constexpr int64_t kMaxPositions = int64_t(1) << 30;  // of a sequence
+constexpr int64_t kMaxStride = int64_t(1) << 36;  // 2^22 tokens of 4 bytes: offsets stay within 64 bits
+constexpr int64_t kMaxRopeStride = int64_t(1) << 28;  // 2^31 tokens
+
 int64_t elem_bytes(mxq_out_t t) { return t == MXQ_OUT_BF16 ? 2 : 4; }
 bool out_type(mxq_out_t t) { return t == MXQ_OUT_F32 || t == MXQ_OUT_BF16; }
 
@@ -46,9 +51,10 @@ bool cache_align_ok(const mxq_kv_cache_t& c, const mxq_kv_seqs_t& s) {
 }
 
 bool cache_supported(const mxq_kv_cache_t& c, const mxq_kv_seqs_t& s, int64_t tokens, int64_t heads) {
-    return tokens <= kMaxTokens && heads <= 65536 && c.num_pages <= kMaxInt && c.page_size >= 16 &&
+    return tokens <= kMaxTokens && heads <= 65536 && tokens * heads <= kMaxRows &&
+           s.seqs * c.kv_heads <= kMaxRows / 8 && c.num_pages <= kMaxInt && c.page_size >= 16 &&
            c.page_size <= MXQ_KV_MAX_PAGE && (c.head_dim == 64 || c.head_dim == 128 || c.head_dim == 256) &&
-           s.seqs <= MXQ_KV_MAX_SEQS && s.max_pages <= kMaxInt / c.page_size && s.table_stride <= kMaxInt;
+           s.seqs <= MXQ_KV_MAX_SEQS && s.max_pages <= kMaxPositions / c.page_size && s.table_stride <= kMaxInt;
 }
 
 int log2_of(int64_t v) {
@@ -68,8 +74,6 @@ mxq::KvSeqs seqs_of(const mxq_kv_seqs_t& s) {
 
 bool stride_ok(int64_t stride, int64_t heads, int64_t dim) { return stride >= heads * dim; }
 bool stride_aligned(int64_t stride, int64_t bytes) { return stride * bytes % 16 == 0; }
-constexpr int64_t kMaxStride = int64_t(1) << 36;  // 2^22 tokens of 4 bytes: offsets stay within 64 bits
-constexpr int64_t kMaxRopeStride = int64_t(1) << 28;  // 2^31 tokens
 
 }  // namespace
 

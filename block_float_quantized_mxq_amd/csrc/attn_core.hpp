@@ -1,0 +1,212 @@
+// attn_core.hpp -- what the two attention kernels (attn_chunk.hip for tiles of
+// many query rows, attn_decode.hip for few) share: which rows and keys a
+// workgroup owns, the split of the keys, and the partial results.
+//
+// A row is one query head of one new token; the rows of a sequence that share
+// a key/value head are numbered r = token * group + head in group, so that all
+// of them read a key once.
+#pragma once
+
+#include "kv_device.hpp"
+
+namespace mxq {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Rows of one sequence and key/value head up to which the decode kernel takes
+// it; above, the chunk kernel does.
+constexpr int kFewRows = 16;
+// Key tiles are split in multiples of this many positions.
+constexpr int kSplitUnit = 64;
+
+struct AttnPlan {
+    int group;      // query heads per key/value head
+    float c;        // |scale| * log2 e: scores are kept in powers of two
+    int q_sign;     // -1, 0, 1: the sign of scale, applied to the queries
+    int splits;     // shares of the keys of a sequence, at most
+    int least;      // positions of a share, at least; a multiple of kSplitUnit
+    int filter;     // 1: this kernel takes only the sequences on its side of kFewRows
+    float* part_o;  // [splits][tokens * heads][dim] unnormalised sums
+    float* part_m;  // [splits][tokens * heads] running maxima (powers of two)
+    float* part_l;  // [splits][tokens * heads] sums of weights
+};
+
+// A sequence's new tokens as the kernels use them: rows t0 .. t0 + n - 1 of
+// the token-major tensors, the first at position pos.  Whatever the metadata
+// holds, the rows lie inside the tensors.
+struct Seq {
+    int t0, n;
+    int64_t pos;
+};
+__device__ __forceinline__ Seq sequence(const KvSeqs& q, int64_t tokens, int s) {
+    const int t0 = q.cu_q[s], t1 = q.cu_q[s + 1];
+    Seq r;
+    r.t0 = t0;
+    const int64_t n = t0 < 0 ? 0 : (int64_t)(t1 < tokens ? t1 : tokens) - t0;
+    r.n = n > 0 ? (int)n : 0;
+    r.pos = (int64_t)q.lens[s] - ((int64_t)t1 - t0);
+    return r;
+}
+
+// The rows that a kernel takes of a sequence of n new tokens.
+template <bool FEW>
+__device__ __forceinline__ int rows_taken(const AttnPlan& p, int n) {
+    const int rows = n * p.group;
+    return (p.filter && (rows <= kFewRows) != FEW) ? 0 : rows;
+}
+
+// Tile `index` of the tiles of BM rows of all sequences: its sequence, and its
+// number there.  One sequence per lane, 64 at a time.
+template <int BM, bool FEW>
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, const AttnPlan& p, int index, int* seq, int* tile) {
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int base = 0; base < a.seqs.seqs; base += 64) {
+        int n = 0;
+        if (base + lane < a.seqs.seqs) {
+            const int t0 = a.seqs.cu_q[base + lane], t1 = a.seqs.cu_q[base + lane + 1];
+            const int64_t m = t0 < 0 ? 0 : (int64_t)(t1 < a.tokens ? t1 : a.tokens) - t0;
+            n = (rows_taken<FEW>(p, m > 0 ? (int)m : 0) + BM - 1) / BM;
+        }
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int up = __shfl_up(sum, d, 64);
+            sum += lane >= d ? up : 0;
+        }
+        const uint64_t past = __ballot(before + sum > index);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            *seq = __builtin_amdgcn_readfirstlane(base + l);
+            *tile = __builtin_amdgcn_readfirstlane(index - before - (__shfl(sum, l, 64) - __shfl(n, l, 64)));
+            return true;
+        }
+        before += __shfl(sum, 63, 64);
+    }
+    return false;
+}
+
+// Positions of a sequence that its new tokens see, [lo, hi) with lo on a
+// kSplitUnit boundary, and their shares: of one length, a multiple of
+// kSplitUnit, at most `splits` of them.
+struct Span {
+    int lo, hi, share, shares;
+};
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const AttnPlan& p, const Seq& s) {
+    const int64_t cap = (int64_t)a.seqs.max_pages << a.cache.page_shift;
+    int64_t hi = s.pos + s.n;
+    hi = hi < 0 ? 0 : hi > cap ? cap : hi;
+    int64_t lo = a.window > 0 ? s.pos - a.window + 1 : 0;
+    lo = lo < 0 ? 0 : lo > hi ? hi : lo;
+    Span r;
+    r.hi = (int)hi;
+    r.lo = (int)lo & ~(kSplitUnit - 1);
+    const int units = (r.hi - r.lo + kSplitUnit - 1) / kSplitUnit;
+    int per = (units + p.splits - 1) / p.splits;
+    if (per < p.least / kSplitUnit) per = p.least / kSplitUnit;
+    r.share = per * kSplitUnit;
+    r.shares = (units + per - 1) / per;
+    return r;
+}
+
+// Positions [lo, hi) that the token at position p sees.
+__device__ __forceinline__ void seen_by(const AttnArgs& a, int64_t p, int cap, int* lo, int* hi) {
+    const int64_t h = p + 1 < 0 ? 0 : p + 1 > cap ? cap : p + 1;
+    int64_t l = a.window > 0 ? p - a.window + 1 : 0;
+    l = l < 0 ? 0 : l > h ? h : l;
+    *lo = (int)l;
+    *hi = (int)h;
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Maximum and sum over the two halves of a wave (lane l and l + 32), and over
+// pairs of 16-lane rows (l and l ^ 16); every lane ends with the result, in a
+// fixed order of operands.  (A vector's element goes through a variable before
+// it is bit-cast: the compiler takes element 0 otherwise.)
+__device__ __forceinline__ float max_halves(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+__device__ __forceinline__ float max_rows16(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ __forceinline__ float sum_rows16(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// 4 bf16 of a column of a row-major LDS tile: each 16-lane group reads a
+// 4 x 16 block (lane l its elements 4 (l % 4) .. of row l / 4) and lane l gets
+// column l of the 4 rows.
+__device__ __forceinline__ u32x2_t read_column4(const void* lds) {
+    typedef __attribute__((address_space(3))) s16x4* p3;
+    return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((p3)(lds)));
+}
+
+// Zeroes the bf16 in v that are infinite or NaN; whether there were any.
+__device__ __forceinline__ bool take_out_not_finite(u32x4_t& v) {
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool lo = (v[i] & 0x7F80u) == 0x7F80u, hi = (v[i] & 0x7F800000u) == 0x7F800000u;
+        v[i] &= (lo ? 0u : 0x0000FFFFu) | (hi ? 0u : 0xFFFF0000u);
+        any |= lo | hi;
+    }
+    return any;
+}
+
+// 8 E4M3 codes (two dwords) with their block's E8M0 byte -> 8 bf16.
+__device__ __forceinline__ u32x4_t mx8_to_bf16(uint32_t c0, uint32_t c1, float sexp) {
+    const uint32_t c[2] = {c0, c1};
+    uint32_t p[4];
+    decode_dwords_scaled<kMXFP8, 2>(c, sexp, p);
+    return u32x4_t{p[0], p[1], p[2], p[3]};
+}
+
+// Elements e .. e + 3 (e a multiple of 4) of a row of the cache's values where
+// they are infinite or NaN and the caller's row sees them, else 0.
+template <int FMT>
+__device__ __forceinline__ f32x4 not_finite_part(const void* v, const uint8_t* scales, int64_t row, int dim, int e,
+                                                 bool sees) {
+    u32x2_t w;
+    if constexpr (FMT == kKvBf16) {
+        w = *reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(v) + row * dim + e);
+    } else {
+        const uint32_t c = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(v) + row * dim + e);
+        const u32x4_t d = mx8_to_bf16(c, 0u, e8m0_exponent(scales[row * (dim / 32) + e / 32]));
+        w = u32x2_t{d[0], d[1]};
+    }
+    f32x4 x = {bf16_lo_to_f32(w[0]), bf16_hi_to_f32(w[0]), bf16_lo_to_f32(w[1]), bf16_hi_to_f32(w[1])};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float e = x[i];
+        const uint32_t b = __builtin_bit_cast(uint32_t, e);
+        x[i] = __builtin_bit_cast(float, (sees & ((b & 0x7F800000u) == 0x7F800000u)) ? b : 0u);
+    }
+    return x;
+}
+
+bool launch_attn_chunk(const AttnArgs& a, const AttnPlan& p, hipStream_t st);
+bool launch_attn_decode(const AttnArgs& a, const AttnPlan& p, hipStream_t st);
+
+// Rows per workgroup of the chunk kernel; the decode kernel's is kFewRows.
+constexpr int kChunkRows = 128;
+
+}  // namespace mxq

@@ -136,8 +136,8 @@ mxq_status_t mxq_rope(const void *x, mxq_out_t x_dtype, void *y, mxq_out_t y_dty
  *              positions p in the cache
  *   head_dim   64, 128 or 256;  page_size a power of two, 16 ..
  *              MXQ_KV_MAX_PAGE;  seqs up to MXQ_KV_MAX_SEQS;  tokens up to
- *              2^22;  heads up to 65536;  strides up to 2^36;  max_pages *
- *              page_size < 2^31;  strides and pointers as in mxq_rope
+ *              2^22;  heads up to 65536;  tokens * heads up to 2^25, seqs *
+ *              kv_heads up to 2^22;  strides up to 2^36;  max_pages * page_size up to 2^30;  strides and pointers as in mxq_rope
  * A token whose p is negative or beyond the table, or whose page is outside
  * [0, num_pages), stores nothing in the cache (its query is still rotated).
  * Two sequences that append to one page must not do so at the same row.

@@ -135,6 +135,8 @@ def test_attention_refusals():
         assert attn(**{a: A + 8}) == ALIGN, a
     assert attn(lse=A + 2) == ALIGN and attn(qs=260) == ALIGN and attn(cu=A + 1) == ALIGN
     assert attn(tokens=(1 << 22) + 1) == UNSUPPORTED and attn(dim=32, qs=128) == UNSUPPORTED
+    assert attn(tokens=(1 << 23) // 4 + 1, heads=16, qs=1024) == UNSUPPORTED  # more than 2^25 query rows
+    assert attn(seqs=4096, hk=2048, heads=2048, qs=2048 * 64) == UNSUPPORTED
     assert attn(window=1 << 31) == UNSUPPORTED and attn(seqs=5000) == UNSUPPORTED
 
 
