@@ -79,8 +79,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
     if (!find_tile<kChunkRows, false>(a, plan, index, &sid, &tile)) return;
     const Seq seq = sequence(a.seqs, a.tokens, sid);
     const Span span = span_of(a, plan, seq);
+    int shares;
+    const int share = share_of(plan, span, &shares);
     const int z = blockIdx.y;
-    if (z > 0 && z >= span.shares) return;
+    if (z > 0 && z >= shares) return;
 
     const int g = plan.group, rows = seq.n * g;
     const int first = tile * kChunkRows, last = (first + kChunkRows < rows ? first + kChunkRows : rows) - 1;
@@ -89,8 +91,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
     int lo_out, hi_in, lo_in, hi_out;
     seen_by(a, seq.pos + first / g, cap, &lo_out, &hi_in);
     seen_by(a, seq.pos + last / g, cap, &lo_in, &hi_out);
-    const int begin = span.lo + z * span.share;
-    int end = begin + span.share < span.hi ? begin + span.share : span.hi;
+    const int begin = span.lo + z * share;
+    int end = begin + share < span.hi ? begin + share : span.hi;
     if (end > hi_out) end = hi_out;
     int t0 = begin;  // first tile of this workgroup
     if (lo_out > t0) t0 = lo_out & ~(kKeys - 1);
@@ -343,7 +345,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
     l = sum_halves(l);
     if (!live) return;
     const int64_t at = token * a.heads + head;
-    if (span.shares <= 1) {
+    if (shares <= 1) {
         const bool empty = hi <= lo;
         const float inv = empty ? 0.0f : 1.0f / l;
         uint16_t* dst = a.out + at * D + 4 * half;

@@ -26,12 +26,13 @@ struct AttnPlan {
     int group;      // query heads per key/value head
     float c;        // |scale| * log2 e: scores are kept in powers of two
     int q_sign;     // -1, 0, 1: the sign of scale, applied to the queries
-    int splits;     // shares of the keys of a sequence, at most
+    int splits;     // chunk kernel: shares of the keys of a sequence, at most
+    int target;     // decode kernel: workgroups to split the work of a call into, about
     int least;      // positions of a share, at least; a multiple of kSplitUnit
     int filter;     // 1: this kernel takes only the sequences on its side of kFewRows
-    float* part_o;  // [splits][tokens * heads][dim] unnormalised sums
-    float* part_m;  // [splits][tokens * heads] running maxima (powers of two)
-    float* part_l;  // [splits][tokens * heads] sums of weights
+    float* part_o;  // unnormalised sums of the shares: chunk [splits][tokens * heads][dim], decode [slot][16][dim]
+    float* part_m;  // their running maxima (powers of two)
+    float* part_l;  // their sums of weights
 };
 
 // A sequence's new tokens as the kernels use them: rows t0 .. t0 + n - 1 of
@@ -58,6 +59,18 @@ __device__ __forceinline__ int rows_taken(const AttnPlan& p, int n) {
     return (p.filter && (rows <= kFewRows) != FEW) ? 0 : rows;
 }
 
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // last lane of rows 0, 2 into rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // lane 31 into the upper half
+    return v;
+}
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
 // Tile `index` of the tiles of BM rows of all sequences: its sequence, and its
 // number there.  One sequence per lane, 64 at a time.
 template <int BM, bool FEW>
@@ -71,29 +84,23 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, const AttnPlan& p, 
             const int64_t m = t0 < 0 ? 0 : (int64_t)(t1 < a.tokens ? t1 : a.tokens) - t0;
             n = (rows_taken<FEW>(p, m > 0 ? (int)m : 0) + BM - 1) / BM;
         }
-        int sum = n;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int up = __shfl_up(sum, d, 64);
-            sum += lane >= d ? up : 0;
-        }
+        const int sum = wave_scan(n);
         const uint64_t past = __ballot(before + sum > index);
         if (past) {
             const int l = __builtin_ctzll(past);
-            *seq = __builtin_amdgcn_readfirstlane(base + l);
-            *tile = __builtin_amdgcn_readfirstlane(index - before - (__shfl(sum, l, 64) - __shfl(n, l, 64)));
+            *seq = base + l;
+            *tile = index - before - (lane_value(sum, l) - lane_value(n, l));
             return true;
         }
-        before += __shfl(sum, 63, 64);
+        before += lane_value(sum, 63);
     }
     return false;
 }
 
-// Positions of a sequence that its new tokens see, [lo, hi) with lo on a
-// kSplitUnit boundary, and their shares: of one length, a multiple of
-// kSplitUnit, at most `splits` of them.
+// Positions of a sequence that its new tokens see, [lo, hi), with lo on a
+// kSplitUnit boundary.
 struct Span {
-    int lo, hi, share, shares;
+    int lo, hi;
 };
 __device__ __forceinline__ Span span_of(const AttnArgs& a, const AttnPlan& p, const Seq& s) {
     const int64_t cap = (int64_t)a.seqs.max_pages << a.cache.page_shift;
@@ -101,15 +108,78 @@ __device__ __forceinline__ Span span_of(const AttnArgs& a, const AttnPlan& p, co
     hi = hi < 0 ? 0 : hi > cap ? cap : hi;
     int64_t lo = a.window > 0 ? s.pos - a.window + 1 : 0;
     lo = lo < 0 ? 0 : lo > hi ? hi : lo;
-    Span r;
-    r.hi = (int)hi;
-    r.lo = (int)lo & ~(kSplitUnit - 1);
-    const int units = (r.hi - r.lo + kSplitUnit - 1) / kSplitUnit;
+    return {(int)lo & ~(kSplitUnit - 1), (int)hi};
+}
+
+// The chunk kernel's split of a sequence's positions: shares of one length, a
+// multiple of kSplitUnit, at most plan.splits of them.
+__device__ __forceinline__ int share_of(const AttnPlan& p, const Span& s, int* shares) {
+    const int units = (s.hi - s.lo + kSplitUnit - 1) / kSplitUnit;
     int per = (units + p.splits - 1) / p.splits;
     if (per < p.least / kSplitUnit) per = p.least / kSplitUnit;
-    r.share = per * kSplitUnit;
-    r.shares = (units + per - 1) / per;
-    return r;
+    *shares = (units + per - 1) / per;
+    return per * kSplitUnit;
+}
+
+// The decode kernel's split: every share of every sequence has the same length,
+// that of the call's tiles of 16 rows times their positions divided by
+// plan.target (but plan.least at least), so that workgroups carry equal work
+// whatever the lengths are.  A call has at most plan.target / kv_heads + tiles
+// shares; those of tiles that are split (at most 2 plan.target / kv_heads) have
+// a slot each for their partial result.
+struct Work {
+    int sid, tile, z;     // sequence, tile of it, share of the tile
+    int shares, share;    // of the tile; their length
+    int slot;             // first share's slot of the tile; -1: not split
+};
+// Share `index` of the call's shares (BY_TILE: the tile `index` of its tiles).
+template <bool BY_TILE>
+__device__ __forceinline__ bool find_work(const AttnArgs& a, const AttnPlan& p, int index, Work* w) {
+    const int lane = threadIdx.x & 63;
+    // (tiles, units of the positions) of this lane's sequence
+    auto load = [&](int base, int* tiles, int* units) __attribute__((always_inline)) {
+        *tiles = *units = 0;
+        if (base + lane < a.seqs.seqs) {
+            const Seq s = sequence(a.seqs, a.tokens, base + lane);
+            const Span span = span_of(a, p, s);
+            *tiles = (rows_taken<true>(p, s.n) + kFewRows - 1) / kFewRows;
+            *units = (span.hi - span.lo + kSplitUnit - 1) / kSplitUnit;
+        }
+    };
+    int tiles0, units0;  // the first 64 sequences' stay in registers
+    load(0, &tiles0, &units0);
+    float total = 0.0f;
+    for (int base = 0; base < a.seqs.seqs; base += 64) {
+        int tiles = tiles0, units = units0;
+        if (base) load(base, &tiles, &units);
+        total += group_sum<64>((float)tiles * (float)units);
+    }
+    int per = __builtin_amdgcn_readfirstlane(
+        (int)__builtin_fminf(__builtin_ceilf(total * (float)a.cache.heads / (float)p.target), 16777216.0f));
+    if (per < p.least / kSplitUnit) per = p.least / kSplitUnit;
+    int before = 0, slots = 0;
+    for (int base = 0; base < a.seqs.seqs; base += 64) {
+        int tiles = tiles0, units = units0;
+        if (base) load(base, &tiles, &units);
+        const int shares = units > per ? (units + per - 1) / per : 1;
+        const int n = BY_TILE ? tiles : tiles * shares, used = shares > 1 ? tiles * shares : 0;
+        const int sum = wave_scan(n), sum_used = wave_scan(used);
+        const uint64_t past = __ballot(before + sum > index);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            const int at = index - before - (lane_value(sum, l) - lane_value(n, l));
+            w->sid = base + l;
+            w->shares = lane_value(shares, l);
+            w->share = per * kSplitUnit;
+            w->tile = BY_TILE ? at : at / w->shares;
+            w->z = BY_TILE ? 0 : at - w->tile * w->shares;
+            w->slot = w->shares > 1 ? slots + lane_value(sum_used, l) - lane_value(used, l) + w->tile * w->shares : -1;
+            return true;
+        }
+        before += lane_value(sum, 63);
+        slots += lane_value(sum_used, 63);
+    }
+    return false;
 }
 
 // Positions [lo, hi) that the token at position p sees.
@@ -201,6 +271,15 @@ __device__ __forceinline__ f32x4 not_finite_part(const void* v, const uint8_t* s
         x[i] = __builtin_bit_cast(float, (sees & ((b & 0x7F800000u) == 0x7F800000u)) ? b : 0u);
     }
     return x;
+}
+
+// Tiles of the decode kernel, at most (a sequence that passes the filter is
+// one tile), and their shares.
+inline int64_t decode_tiles(const AttnArgs& a, const AttnPlan& p) {
+    return p.filter ? a.seqs.seqs : a.tokens * p.group / kFewRows + a.seqs.seqs;
+}
+inline int64_t decode_shares(const AttnArgs& a, const AttnPlan& p) {
+    return decode_tiles(a, p) + p.target / a.cache.heads + 1;
 }
 
 bool launch_attn_chunk(const AttnArgs& a, const AttnPlan& p, hipStream_t st);

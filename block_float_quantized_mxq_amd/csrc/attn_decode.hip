@@ -22,7 +22,7 @@ constexpr int kBlock = 32;  // positions per wave and step
 constexpr float kDecodeSlack = 8.0f;
 
 template <int D, int FMT>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_decode_kernel(AttnArgs a, AttnPlan plan) {
+__global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void attn_decode_kernel(AttnArgs a, AttnPlan plan) {
     constexpr int KSTEPS = D / 32;                       // MFMA steps of the first product
     constexpr int DB = D / 16;                           // 16-row blocks of O^T
     constexpr bool MX = FMT == kKvMxfp8;
@@ -39,12 +39,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_decode_kernel(Attn
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int col = lane & 15, quad = lane >> 4;
     const int kvh = (int)(blockIdx.x % (unsigned)a.cache.heads);
-    int sid, tile;
-    if (!find_tile<kFewRows, true>(a, plan, (int)(blockIdx.x / (unsigned)a.cache.heads), &sid, &tile)) return;
+    Work work;
+    if (!find_work<false>(a, plan, (int)(blockIdx.x / (unsigned)a.cache.heads), &work)) return;
+    const int sid = work.sid, tile = work.tile;
     const Seq seq = sequence(a.seqs, a.tokens, sid);
     const Span span = span_of(a, plan, seq);
-    const int z = blockIdx.y;
-    if (z > 0 && z >= span.shares) return;
 
     const int g = plan.group, rows = seq.n * g;
     const int first = tile * kFewRows, last = (first + kFewRows < rows ? first + kFewRows : rows) - 1;
@@ -52,8 +51,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_decode_kernel(Attn
     int lo_out, hi_in, lo_in, hi_out;
     seen_by(a, seq.pos + first / g, cap, &lo_out, &hi_in);
     seen_by(a, seq.pos + last / g, cap, &lo_in, &hi_out);
-    const int begin = span.lo + z * span.share;
-    int end = begin + span.share < span.hi ? begin + span.share : span.hi;
+    const int begin = span.lo + work.z * work.share;
+    int end = begin + work.share < span.hi ? begin + work.share : span.hi;
     if (end > hi_out) end = hi_out;
     const bool mixed = hi_in != hi_out || lo_in != lo_out;  // rows that see different positions
 
@@ -279,20 +278,21 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_decode_kernel(Attn
     seen_by(a, seq.pos + t, cap, &rlo, &rhi);
     const bool empty = rhi <= rlo;
     const float inv = empty ? 0.0f : 1.0f / total;
-    const int64_t slot = (int64_t)z * a.tokens * a.heads + at;
+    // row of the partial results
+    const int64_t slot = ((int64_t)(work.slot + work.z) * a.cache.heads + kvh) * kFewRows + row;
 #pragma unroll
     for (int e = 4 * part; e < D; e += 64) {
         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int w = 0; w < 4; ++w)
             if (weight[w] != 0.0f) x += weight[w] * *reinterpret_cast<const f32x4*>(sums + (w * kFewRows + row) * kRow + e);
-        if (span.shares <= 1)
+        if (work.slot < 0)
             *reinterpret_cast<u32x2_t*>(a.out + at * D + e) = u32x2_t{pack_bf16(x[0] * inv, x[1] * inv), pack_bf16(x[2] * inv, x[3] * inv)};
         else
             *reinterpret_cast<f32x4*>(plan.part_o + slot * D + e) = x;
     }
     if (part == 0) {
-        if (span.shares <= 1) {
+        if (work.slot < 0) {
             if (a.lse) a.lse[at] = empty ? -__builtin_inff() : (top + __builtin_amdgcn_logf(total)) * 0.69314718055994531f;
         } else {
             plan.part_m[slot] = top;
@@ -303,8 +303,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_decode_kernel(Attn
 
 template <int D>
 static void launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-    const int64_t tiles = a.tokens * p.group / kFewRows + a.seqs.seqs;
-    const dim3 grid((unsigned)(tiles * a.cache.heads), (unsigned)p.splits), block(256);
+    const dim3 grid((unsigned)(decode_shares(a, p) * a.cache.heads)), block(256);
     if (a.cache.fmt == kKvMxfp8) hipLaunchKernelGGL((attn_decode_kernel<D, kKvMxfp8>), grid, block, 0, st, a, p);
     else hipLaunchKernelGGL((attn_decode_kernel<D, kKvBf16>), grid, block, 0, st, a, p);
 }

@@ -11,119 +11,186 @@
 
 namespace mxq {
 
-constexpr int kMaxSplits = 256;
+constexpr int kMaxSplits = 32;   // of the chunk kernel
 constexpr int kDesignCus = 256;  // compute units the split is sized for
 
-// Joins what one of the two kernels left: one wave per row; lane z % 64 holds
-// share z's statistics.
-template <bool FEW>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, AttnPlan p) {
-    const int lane = threadIdx.x & 63;
-    const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-    if (row >= a.tokens * a.heads) return;
-    const int t = (int)(row / a.heads);
-    const int sid = sequence_of(a.seqs, t);
-    if (sid >= a.seqs.seqs || t < a.seqs.cu_q[0]) return;
-    const Seq seq = sequence(a.seqs, a.tokens, sid);
-    if (t < seq.t0 || t - seq.t0 >= seq.n) return;
-    if (rows_taken<FEW>(p, seq.n) == 0) return;
-    const Span span = span_of(a, p, seq);
-    if (span.shares <= 1) return;  // written by the kernel itself
+__device__ __forceinline__ void write_row(const AttnArgs& a, int64_t at, int dim, int e, const f32x4& sum, float top,
+                                          float total, bool empty) {
+    const float inv = empty ? 0.0f : 1.0f / total;
+    *reinterpret_cast<u32x2_t*>(a.out + at * dim + e) =
+        u32x2_t{pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv)};
+    if (a.lse && e == 0) a.lse[at] = empty ? -__builtin_inff() : (top + __builtin_amdgcn_logf(total)) * 0.69314718055994531f;
+}
+
+// A share's weight in the join; a share that summed nothing has none, and its
+// sums were not written.
+__device__ __forceinline__ float share_weight(float m, float l, float top) { return l == 0.0f ? 0.0f : exp2_hw(m - top); }
+
+__device__ __forceinline__ bool sees_nothing(const AttnArgs& a, const Seq& seq, int tok) {
+    int lo, hi;
+    seen_by(a, seq.pos + tok, (int)((int64_t)a.seqs.max_pages << a.cache.page_shift), &lo, &hi);
+    return hi <= lo;
+}
+
+// Join of the chunk kernel's shares: a thread takes 4 elements of a row and
+// adds its few shares up in order.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_chunk_kernel(AttnArgs a, AttnPlan p) {
+    constexpr int LANES = D / 4, R = 256 / LANES;
+    const int64_t at = (int64_t)blockIdx.x * R + threadIdx.x / LANES;
     const int64_t step = a.tokens * a.heads;
-    float m[kMaxSplits / 64], l[kMaxSplits / 64], top = -__builtin_inff();
-#pragma unroll
-    for (int i = 0; i < kMaxSplits / 64; ++i) {
-        const int z = 64 * i + lane;
-        m[i] = -__builtin_inff();
-        l[i] = 0.0f;
-        if (z < span.shares) {
-            m[i] = p.part_m[z * step + row];
-            l[i] = p.part_l[z * step + row];
-        }
-        top = __builtin_fmaxf(top, m[i]);
+    // the rows of a wave may lie in different sequences: one after the other
+    const int64_t last = (int64_t)blockIdx.x * R + (threadIdx.x | 63) / LANES;
+    int sid = -1;
+    for (int64_t row = (int64_t)blockIdx.x * R + (threadIdx.x & ~63) / LANES; row <= last; ++row) {
+        const int s = row < step ? sequence_of(a.seqs, (int)(row / a.heads)) : a.seqs.seqs;
+        if (row == at) sid = s;
     }
-    top = max_halves(max_rows16(top));
-    top = __builtin_fmaxf(top, dpp_f32<kDppQuadXor1>(top));
-    top = __builtin_fmaxf(top, dpp_f32<kDppQuadXor2>(top));
-    top = __builtin_fmaxf(top, dpp_f32<kDppRowHalfMirror>(top));
-    top = __builtin_fmaxf(top, dpp_f32<kDppRowMirror>(top));
+    const int t = (int)(at / a.heads);
+    if (at >= step || sid >= a.seqs.seqs) return;
+    const Seq seq = sequence(a.seqs, a.tokens, sid);
+    if (t < seq.t0 || t - seq.t0 >= seq.n || rows_taken<false>(p, seq.n) == 0) return;
+    int shares;
+    share_of(p, span_of(a, p, seq), &shares);
+    if (shares <= 1) return;  // written by the kernel itself
+    const int e = 4 * (threadIdx.x % LANES);
+    float m[kMaxSplits], top = -__builtin_inff();
+#pragma unroll
+    for (int z = 0; z < kMaxSplits; ++z) {
+        m[z] = z < shares ? p.part_m[z * step + at] : -__builtin_inff();
+        top = __builtin_fmaxf(top, m[z]);
+    }
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
     float total = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kMaxSplits / 64; ++i) {
-        m[i] = l[i] == 0.0f ? 0.0f : exp2_hw(m[i] - top);  // the share's weight
-        total += l[i] == 0.0f ? 0.0f : m[i] * l[i];
-    }
-    total = group_sum<64>(total);
-    const int dim = a.cache.dim, each = dim / 64;  // adjacent elements per lane: 1, 2 or 4
-    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kMaxSplits / 64; ++i) {
-        const int n = span.shares - 64 * i < 64 ? span.shares - 64 * i : 64;
-        for (int z = 0; z < n; ++z) {
-            const float w = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, m[i]), z));
-            if (w == 0.0f) continue;  // nothing was summed there
-            const float* src = p.part_o + ((64 * i + z) * step + row) * dim + lane * each;
-            if (each == 1) {
-                o[0] += w * src[0];
-            } else if (each == 2) {
-                const f32x2_t x = *reinterpret_cast<const f32x2_t*>(src);
-                o[0] += w * x[0];
-                o[1] += w * x[1];
-            } else {
-                const f32x4 x = *reinterpret_cast<const f32x4*>(src);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) o[j] += w * x[j];
+    for (int z = 0; z < kMaxSplits; ++z) {
+        if (z < shares) {
+            const float l = p.part_l[z * step + at], w = share_weight(m[z], l, top);
+            const f32x4 x = *reinterpret_cast<const f32x4*>(p.part_o + (z * step + at) * D + e);
+            if (l != 0.0f) {
+                sum += w * x;
+                total += w * l;
             }
         }
     }
-    const int cap = (int)((int64_t)a.seqs.max_pages << a.cache.page_shift);
-    int lo, hi;
-    seen_by(a, seq.pos + (t - seq.t0), cap, &lo, &hi);
-    const bool empty = hi <= lo;
-    const float inv = empty ? 0.0f : 1.0f / total;
-    uint16_t* dst = a.out + row * dim + lane * each;
-    if (each == 1) {
-        dst[0] = (uint16_t)pack_bf16(o[0] * inv, 0.0f);
-    } else {
-        *reinterpret_cast<uint32_t*>(dst) = pack_bf16(o[0] * inv, o[1] * inv);
-        if (each == 4) *reinterpret_cast<uint32_t*>(dst + 2) = pack_bf16(o[2] * inv, o[3] * inv);
+    write_row(a, at, D, e, sum, top, total, sees_nothing(a, seq, t - seq.t0));
+}
+
+// Join of the decode kernel's shares: a workgroup takes a row, D / 4 threads
+// its elements and 256 / (D / 4) groups of them every so many shares.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_decode_kernel(AttnArgs a, AttnPlan p) {
+    constexpr int LANES = D / 4, G = 256 / LANES, U = 4;
+    __shared__ f32x4 sums[G][LANES];
+    __shared__ float stat[2][G];
+    const int heads = a.cache.heads, kvh = (int)(blockIdx.x % (unsigned)heads);
+    Work w;
+    if (!find_work<true>(a, p, (int)(blockIdx.x / (unsigned)heads), &w) || w.slot < 0) return;
+    const Seq seq = sequence(a.seqs, a.tokens, w.sid);
+    const int first = w.tile * kFewRows, rows = seq.n * p.group - first;
+    const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    const int64_t step = (int64_t)heads * kFewRows;
+    for (int r = blockIdx.y; r < rows && r < kFewRows; r += gridDim.y) {
+        const int64_t base = ((int64_t)w.slot * heads + kvh) * kFewRows + r;
+        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        float top = -__builtin_inff(), total = 0.0f;
+        for (int z0 = group; z0 < w.shares; z0 += G * U) {
+            f32x4 x[U];
+            float m[U], l[U], next = top;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool in = z0 + u * G < w.shares;
+                const int64_t at = base + (in ? z0 + u * G : z0) * step;
+                x[u] = *reinterpret_cast<const f32x4*>(p.part_o + at * D + 4 * lane);
+                m[u] = p.part_m[at];
+                l[u] = in ? p.part_l[at] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) next = l[u] == 0.0f ? next : __builtin_fmaxf(next, m[u]);
+            const float keep = next == top ? 1.0f : exp2_hw(top - next);
+            sum *= keep;
+            total *= keep;
+            top = next;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (l[u] != 0.0f) {
+                    const float v = exp2_hw(m[u] - top);
+                    sum += v * x[u];
+                    total += v * l[u];
+                }
+            }
+        }
+        sums[group][lane] = sum;
+        if (lane == 0) {
+            stat[0][group] = top;
+            stat[1][group] = total;
+        }
+        __syncthreads();
+        if (group == 0) {
+            top = stat[0][0];
+#pragma unroll
+            for (int i = 1; i < G; ++i) top = __builtin_fmaxf(top, stat[0][i]);
+            sum = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < G; ++i) {
+                const float l = stat[1][i];
+                if (l != 0.0f) {
+                    const float v = exp2_hw(stat[0][i] - top);
+                    sum += v * sums[i][lane];
+                    total += v * l;
+                }
+            }
+            const int tok = (first + r) / p.group;
+            const int64_t at = (int64_t)(seq.t0 + tok) * a.heads + kvh * p.group + (first + r - tok * p.group);
+            write_row(a, at, D, 4 * lane, sum, top, total, sees_nothing(a, seq, tok));
+        }
+        __syncthreads();
     }
-    if (a.lse && lane == 0) a.lse[row] = empty ? -__builtin_inff() : (top + __builtin_amdgcn_logf(total)) * 0.69314718055994531f;
+}
+
+template <int D>
+static void launch_join_chunk(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+    const int64_t rows = 1024 / D;
+    const dim3 grid((unsigned)((a.tokens * a.heads + rows - 1) / rows)), block(256);
+    hipLaunchKernelGGL(attn_join_chunk_kernel<D>, grid, block, 0, st, a, p);
+}
+template <int D>
+static void launch_join_decode(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
+    const int64_t most = (a.max_q < a.tokens ? a.max_q : a.tokens) * p.group;
+    const dim3 grid((unsigned)(decode_tiles(a, p) * a.cache.heads), (unsigned)(most < kFewRows ? most : kFewRows)), block(256);
+    hipLaunchKernelGGL(attn_join_decode_kernel<D>, grid, block, 0, st, a, p);
 }
 
 namespace {
 
 struct Choice {
     bool few, many;
-    int few_splits, many_splits;
+    int target;       // workgroups of the decode kernel
+    int many_splits;  // shares of a sequence of the chunk kernel
 };
 
-// Which kernels run, and into how many shares the positions are split at most.
-// max_q is a hint: with every sequence's rows below kFewRows the decode kernel
-// takes all, a single sequence with more goes to the chunk kernel, else both
-// run and each takes its side.
+// Which kernels run, and into how many shares the positions are split.  max_q
+// is a hint: if it puts every sequence's rows below kFewRows the decode kernel
+// takes all; else the chunk kernel runs, and beside it the decode kernel if the
+// number of tokens leaves room for sequences with few.
 Choice choose(int64_t group, int64_t kv_heads, int64_t tokens, int64_t seqs, int64_t positions, int64_t max_q) {
-    const int64_t most = (max_q < tokens ? max_q : tokens) * group;
+    const int64_t most_q = max_q < tokens ? max_q : tokens;
     Choice c{};
-    c.few = most <= kFewRows || seqs > 1;
-    c.many = most > kFewRows;
-    c.few_splits = c.many_splits = 1;
-    if (c.few) {
-        // about 8 workgroups a compute unit, of at least 128 positions each
-        const int64_t tiles = c.many || seqs > tokens * group / kFewRows ? seqs : tokens * group / kFewRows;
-        const int64_t units = tiles * kv_heads;
-        int64_t s = (8 * kDesignCus + units - 1) / units;
-        const int64_t top = (positions + 127) / 128;
-        s = s < top ? s : top;
-        c.few_splits = (int)(s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : s);
-    }
+    c.many = most_q * group > kFewRows;
+    c.few = !c.many || (seqs > 1 && 4 * tokens < 3 * seqs * most_q);
+    // Few tiles: three workgroups are resident on a compute unit, one round of
+    // them; more tiles have other lengths each: more and shorter shares even
+    // out the last round.
+    c.target = (seqs * kv_heads <= 64 ? 3 : 9) * kDesignCus;
+    c.many_splits = 1;
     if (c.many) {
         // two workgroups are resident on a compute unit: the number of shares
         // that fills the last round best, with a price for each share's join
         const int64_t units = ((tokens * group + kChunkRows - 1) / kChunkRows) * kv_heads;
         const int64_t top = (positions + 255) / 256;
         double best = 1e30;
-        for (int64_t s = 1; s <= 32 && s <= top; ++s) {
+        for (int64_t s = 1; s <= kMaxSplits && s <= top; ++s) {
             const double rounds = (double)((units * s + 2 * kDesignCus - 1) / (2 * kDesignCus));
             const double cost = rounds / (double)s * (1.0 + 0.03 * (double)(s - 1));
             if (cost < best) {
@@ -135,18 +202,20 @@ Choice choose(int64_t group, int64_t kv_heads, int64_t tokens, int64_t seqs, int
     return c;
 }
 
-int64_t partial_floats(int64_t splits, int64_t rows, int64_t dim) { return splits > 1 ? splits * rows * (dim + 2) : 0; }
+// Rows of the partial results.  Decode: a split tile has less than twice its
+// part of the target in shares, and a slot each.
+int64_t chunk_rows(const Choice& c, int64_t rows) { return c.many && c.many_splits > 1 ? c.many_splits * rows : 0; }
+int64_t decode_rows(const Choice& c, int64_t kv_heads) { return c.few ? (2 * (c.target / kv_heads) + 2) * kv_heads * kFewRows : 0; }
 
-AttnPlan plan_of(const AttnArgs& a, int splits, int least, bool filter, float* ws) {
+AttnPlan plan_of(const AttnArgs& a, bool filter, int64_t rows, float* ws) {
     AttnPlan p{};
     p.group = (int)(a.heads / a.cache.heads);
     const float mag = a.scale < 0.0f ? -a.scale : a.scale;
     p.c = mag == 0.0f ? 1.0f : mag * 1.44269504088896341f;
     p.q_sign = a.scale > 0.0f ? 1 : a.scale < 0.0f ? -1 : 0;
-    p.splits = splits;
-    p.least = least;
+    p.splits = 1;
+    p.target = 1;
     p.filter = filter ? 1 : 0;
-    const int64_t rows = (int64_t)splits * a.tokens * a.heads;
     p.part_o = ws;
     p.part_m = ws + rows * a.cache.dim;
     p.part_l = p.part_m + rows;
@@ -158,22 +227,38 @@ AttnPlan plan_of(const AttnArgs& a, int splits, int least, bool filter, float* w
 int64_t paged_attn_workspace(int64_t heads, int64_t kv_heads, int64_t dim, int64_t tokens, int64_t seqs,
                              int64_t max_pages, int64_t page_size, int64_t max_q) {
     const Choice c = choose(heads / kv_heads, kv_heads, tokens, seqs, max_pages * page_size, max_q);
-    const int64_t rows = tokens * heads;
-    return 4 * ((c.few ? partial_floats(c.few_splits, rows, dim) : 0) + (c.many ? partial_floats(c.many_splits, rows, dim) : 0));
+    return 4 * (dim + 2) * (chunk_rows(c, tokens * heads) + decode_rows(c, kv_heads));
 }
 
 bool launch_paged_attn(const AttnArgs& a, hipStream_t st) {
-    const int64_t group = a.heads / a.cache.heads;
-    const Choice c = choose(group, a.cache.heads, a.tokens, a.seqs.seqs, (int64_t)a.seqs.max_pages << a.cache.page_shift, a.max_q);
+    const Choice c = choose(a.heads / a.cache.heads, a.cache.heads, a.tokens, a.seqs.seqs,
+                            (int64_t)a.seqs.max_pages << a.cache.page_shift, a.max_q);
     float* ws = static_cast<float*>(a.workspace);
-    const AttnPlan few = plan_of(a, c.few_splits, 128, c.many, ws);
-    if (c.few) ws += partial_floats(c.few_splits, a.tokens * a.heads, a.cache.dim);
-    const AttnPlan many = plan_of(a, c.many_splits, 256, c.few, ws);
-    if (c.many && !launch_attn_chunk(a, many, st)) return false;
-    if (c.few && !launch_attn_decode(a, few, st)) return false;
-    const dim3 grid((unsigned)((a.tokens * a.heads + 3) / 4)), block(256);
-    if (c.many && c.many_splits > 1) hipLaunchKernelGGL(attn_join_kernel<false>, grid, block, 0, st, a, many);
-    if (c.few && c.few_splits > 1) hipLaunchKernelGGL(attn_join_kernel<true>, grid, block, 0, st, a, few);
+    if (c.few) {
+        AttnPlan p = plan_of(a, c.many, decode_rows(c, a.cache.heads), ws);
+        p.target = c.target;
+        p.least = 128;
+        if (!launch_attn_decode(a, p, st)) return false;
+        switch (a.cache.dim) {
+            case 64: launch_join_decode<64>(a, p, st); break;
+            case 128: launch_join_decode<128>(a, p, st); break;
+            case 256: launch_join_decode<256>(a, p, st); break;
+        }
+        ws += decode_rows(c, a.cache.heads) * (a.cache.dim + 2);
+    }
+    if (c.many) {
+        AttnPlan p = plan_of(a, c.few, chunk_rows(c, a.tokens * a.heads), ws);
+        p.splits = c.many_splits;
+        p.least = 256;
+        if (!launch_attn_chunk(a, p, st)) return false;
+        if (c.many_splits > 1) {
+            switch (a.cache.dim) {
+                case 64: launch_join_chunk<64>(a, p, st); break;
+                case 128: launch_join_chunk<128>(a, p, st); break;
+                case 256: launch_join_chunk<256>(a, p, st); break;
+            }
+        }
+    }
     return true;
 }
 

@@ -56,9 +56,15 @@ def bind(L):
         f.restype = I
 
 
+_loaded = None
+
+
 def _lib():
-    from . import lib
-    return lib()
+    global _loaded
+    if _loaded is None:
+        from . import lib
+        _loaded = lib()
+    return _loaded
 
 
 def _check(st, what):
@@ -67,43 +73,53 @@ def _check(st, what):
         raise MxqError(st, what)
 
 
-def _need(t, dtypes, name, device=None):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+_F32, _BF16, _I32, _U8 = torch.float32, torch.bfloat16, torch.int32, torch.uint8
+_X = (_F32, _BF16)
+_Tensor = torch.Tensor
+
+
+# The checks run before every launch, so they are written for the case that passes; _refuse says what was wrong.
+def _refuse(t, dtypes, name, index):
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call's other tensors are on {device}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, the call's other tensors are on cuda:{index}")
 
 
-def _flat(t, dtypes, name, device, shape=None):
-    _need(t, dtypes, name, device)
+def _first(t, dtypes, name):
+    """The device index of the tensor that decides where a call runs."""
+    if not isinstance(t, _Tensor) or not t.is_cuda or t.dtype not in dtypes:
+        _refuse(t, dtypes, name, -1)
+    return t.get_device()
+
+
+def _flat(t, dtype, name, index, shape):
+    if not isinstance(t, _Tensor) or t.dtype is not dtype or t.get_device() != index:
+        _refuse(t, (dtype,), name, index)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t
+    return t.data_ptr()
 
 
-_X = (torch.float32, torch.bfloat16)
-_BF16, _F32, _I32, _U8 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.uint8,)
-
-
-def _heads_of(t, dtypes, name, device=None):
+def _heads_of(t, dtypes, name, index):
     """[tokens, heads, dim] whose heads are adjacent; returns the tokens' stride in elements."""
-    _need(t, dtypes, name, device)
+    if not isinstance(t, _Tensor) or t.dtype not in dtypes or t.get_device() != index:
+        _refuse(t, dtypes, name, index)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
     n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    stride, head, elem = t.stride()
+    if (d > 1 and elem != 1) or (h > 1 and head != d):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.stride(0) if n > 1 else h * d
+    return stride if n > 1 else h * d
 
 
 @contextlib.contextmanager
-def _guard(device, stream):
-    with torch.cuda.device(device):
+def _guard(index, stream):
+    with torch.cuda.device(index):
         if stream is None:
             yield
         else:
@@ -111,17 +127,26 @@ def _guard(device, stream):
                 yield
 
 
-def _on(device, stream):
+_HERE = contextlib.nullcontext()
+
+
+def _on(index, stream):
     """Context in which allocations belong to the call's stream and the call's device is the current one."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    if stream is not None and stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
-    return _guard(device, stream)
+    if stream is None and _current_device() == index:
+        return _HERE
+    if stream is not None and stream.device_index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
+    return _guard(index, stream)
 
 
-def _raw_stream(device, stream):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+# torch's own shortcuts to the current device and stream, without the objects that torch.cuda builds around them
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _raw_stream(index, stream):
+    return _current_raw_stream(index) if stream is None else stream.cuda_stream
 
 
 def _layout(layout):
@@ -130,40 +155,41 @@ def _layout(layout):
     return ROPE_LAYOUTS[layout]
 
 
-def _rope_params(inv_freq, layout, mscale, device):
+def _rope_params(inv_freq, layout, mscale, index):
     code = _layout(layout)
     if inv_freq is None:
         return _Rope(None, 0, code, 1.0)
-    _flat(inv_freq, _F32, "inv_freq", device)
-    if inv_freq.dim() != 1:
-        raise ValueError("inv_freq must have one dimension")
-    return _Rope(inv_freq.data_ptr(), 2 * inv_freq.numel(), code, mscale)
+    p = _flat(inv_freq, _F32, "inv_freq", index, (inv_freq.numel() if isinstance(inv_freq, _Tensor) else 0,))
+    return _Rope(p, 2 * inv_freq.numel(), code, mscale)
 
 
 class KVCache:
     """A paged cache over the caller's tensors: k, v [pages, kv_heads, page_size, head_dim] in bfloat16, or uint8
     E4M3 codes with uint8 E8M0 scales k_scales, v_scales [pages, kv_heads, page_size, head_dim / 32]."""
 
-    __slots__ = ("k", "v", "k_scales", "v_scales", "device", "shape", "format", "_c")
+    __slots__ = ("k", "v", "k_scales", "v_scales", "device", "shape", "format", "_index", "_c", "_ref")
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
         mx = k_scales is not None or v_scales is not None
-        _need(k, _U8 if mx else _BF16, "cache k")
+        dtype = _U8 if mx else _BF16
+        index = _first(k, (dtype,), "cache k")
         if k.dim() != 4:
             raise ValueError("cache k must be [pages, kv_heads, page_size, head_dim]")
         shape = k.shape
-        _flat(k, _U8 if mx else _BF16, "cache k", None)
-        _flat(v, _U8 if mx else _BF16, "cache v", k.device, shape)
+        pages, heads, page, dim = shape
+        kp, vp = _flat(k, dtype, "cache k", index, shape), _flat(v, dtype, "cache v", index, shape)
+        ks = vs = None
         if mx:
-            if shape[3] % 32:
-                raise ValueError(f"head_dim {shape[3]} is not a multiple of the MXFP8 block of 32")
-            want = (*shape[:3], shape[3] // 32)
-            _flat(k_scales, _U8, "cache k_scales", k.device, want)
-            _flat(v_scales, _U8, "cache v_scales", k.device, want)
+            if dim % 32:
+                raise ValueError(f"head_dim {dim} is not a multiple of the MXFP8 block of 32")
+            want = (pages, heads, page, dim // 32)
+            ks = _flat(k_scales, _U8, "cache k_scales", index, want)
+            vs = _flat(v_scales, _U8, "cache v_scales", index, want)
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.device, self.shape, self.format = k.device, tuple(shape), KV_MXFP8 if mx else KV_BF16
-        self._c = _Cache(self.format, 0, k.data_ptr(), v.data_ptr(), k_scales.data_ptr() if mx else None,
-                         v_scales.data_ptr() if mx else None, shape[0], shape[2], shape[1], shape[3])
+        self.device, self.shape, self.format = k.device, shape, KV_MXFP8 if mx else KV_BF16
+        self._index = index
+        self._c = _Cache(self.format, 0, kp, vp, ks, vs, pages, page, heads, dim)
+        self._ref = ctypes.byref(self._c)
 
 
 def kv_cache(pages, kv_heads, page_size, head_dim, fmt="bf16", device="cuda"):
@@ -178,15 +204,17 @@ def kv_cache(pages, kv_heads, page_size, head_dim, fmt="bf16", device="cuda"):
     return KVCache(*parts)
 
 
-def _seqs_of(cache, block_table, cu_q, kv_lens):
-    _need(block_table, _I32, "block_table", cache.device)
-    if block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be [seqs, max_pages] with contiguous rows")
+def _seqs_of(index, block_table, cu_q, kv_lens):
+    if not isinstance(block_table, _Tensor) or block_table.dtype is not _I32 or block_table.get_device() != index:
+        _refuse(block_table, (_I32,), "block_table", index)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [seqs, max_pages]")
     seqs, width = block_table.shape
-    _flat(cu_q, _I32, "cu_q", cache.device, (seqs + 1,))
-    _flat(kv_lens, _I32, "kv_lens", cache.device, (seqs,))
-    return _Seqs(block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), seqs, width,
-                 block_table.stride(0) if seqs > 1 else width)
+    stride, elem = block_table.stride()
+    if width > 1 and elem != 1:
+        raise ValueError("the rows of block_table must be contiguous")
+    return _Seqs(block_table.data_ptr(), _flat(cu_q, _I32, "cu_q", index, (seqs + 1,)),
+                 _flat(kv_lens, _I32, "kv_lens", index, (seqs,)), seqs, width, stride if seqs > 1 else width)
 
 
 def rope_inv_freq(rot_dim, theta=10000.0, scaling=None, factor=1.0, context=0, low=1.0, high=32.0, device="cuda"):
@@ -206,24 +234,24 @@ def rope(x, positions, inv_freq, layout="half", mscale=1.0, out=None, out_dtype=
     """Rotary positions of x [tokens, heads, head_dim] (float32 or bfloat16) -> out_dtype (float32 or bfloat16),
     same shape.  positions int32 [tokens]; the first 2 * len(inv_freq) elements of a head turn.  out may be x
     (in place) if the types agree, else it must not overlap x."""
-    xs = _heads_of(x, _X, "x")
-    dev = x.device
+    index = _first(x, _X, "x")
+    xs = _heads_of(x, _X, "x", index)
     n, h, d = x.shape
-    _flat(positions, _I32, "positions", dev, (n,))
-    r = _rope_params(inv_freq, layout, mscale, dev)
+    pos = _flat(positions, _I32, "positions", index, (n,))
+    r = _rope_params(inv_freq, layout, mscale, index)
     if out is not None:
         out_dtype = out.dtype
     if out_dtype not in _X:
         raise TypeError(f"out must be float32 or bfloat16, got {out_dtype}")
-    with _on(dev, stream):
+    with _on(index, stream):
         if out is None:
-            out = torch.empty((n, h, d), dtype=out_dtype, device=dev)
-        ys = _heads_of(out, _X, "out", dev)
-        if out.shape != x.shape:
-            raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
-        _check(_lib().mxq_rope(x.data_ptr(), x.dtype == torch.bfloat16, out.data_ptr(), out_dtype == torch.bfloat16,
-                               positions.data_ptr(), ctypes.byref(r), n, h, d, xs, ys, _raw_stream(dev, stream)),
-               "mxq_rope")
+            out, ys = torch.empty((n, h, d), dtype=out_dtype, device=x.device), h * d
+        else:
+            ys = _heads_of(out, _X, "out", index)
+            if out.shape != x.shape:
+                raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
+        _check(_lib().mxq_rope(x.data_ptr(), x.dtype is _BF16, out.data_ptr(), out_dtype is _BF16, pos, ctypes.byref(r),
+                               n, h, d, xs, ys, _raw_stream(index, stream)), "mxq_rope")
     return out
 
 
@@ -234,41 +262,39 @@ def kv_append(k, v, cache, block_table, cu_q, kv_lens, q=None, inv_freq=None, la
     float32 or bfloat16.  inv_freq None: nothing turns.  positions int32 [tokens]: what to rotate by (default: the
     tokens' positions in the cache).  Rows outside every sequence are left as they were: in q_out too, which is
     allocated uninitialised when None."""
-    ks = _heads_of(k, _X, "k", cache.device)
-    vs = _heads_of(v, (k.dtype,), "v", cache.device)
-    dev = cache.device
+    index = cache._index
+    ks = _heads_of(k, _X, "k", index)
+    same = (k.dtype,)
+    vs = _heads_of(v, same, "v", index)
     n, hk, d = k.shape
-    if v.shape != k.shape or (hk, d) != (cache.shape[1], cache.shape[3]):
-        raise ValueError(f"k {tuple(k.shape)}, v {tuple(v.shape)} and the cache {cache.shape} disagree")
-    qs, h = 0, hk
+    if v.shape != k.shape or hk != cache._c.kv_heads or d != cache._c.head_dim:
+        raise ValueError(f"k {tuple(k.shape)}, v {tuple(v.shape)} and the cache {tuple(cache.shape)} disagree")
+    qs, h, qp, op, pp = 0, hk, None, None, None
     if q is not None:
-        qs = _heads_of(q, (k.dtype,), "q", dev)
-        h = q.shape[1]
+        qs = _heads_of(q, same, "q", index)
+        h, qp = q.shape[1], q.data_ptr()
         if q.shape[0] != n or q.shape[2] != d:
             raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} disagree")
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    r = _rope_params(inv_freq, layout, mscale, dev)
+    r = _rope_params(inv_freq, layout, mscale, index)
     if positions is not None:
-        _flat(positions, _I32, "positions", dev, (n,))
-    s = _seqs_of(cache, block_table, cu_q, kv_lens)
-    with _on(dev, stream):
+        pp = _flat(positions, _I32, "positions", index, (n,))
+    s = _seqs_of(index, block_table, cu_q, kv_lens)
+    with _on(index, stream):
         if q is not None:
             if q_out is None:
-                q_out = torch.empty((n, h, d), dtype=torch.bfloat16, device=dev)
-            _flat(q_out, _BF16, "q_out", dev, (n, h, d))
-        _check(_lib().mxq_kv_append(None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                    k.dtype == torch.bfloat16, None if q is None else q_out.data_ptr(),
-                                    None if positions is None else positions.data_ptr(), ctypes.byref(r),
-                                    ctypes.byref(cache._c), ctypes.byref(s), n, h, qs, ks, vs,
-                                    _raw_stream(dev, stream)), "mxq_kv_append")
+                q_out = torch.empty((n, h, d), dtype=_BF16, device=cache.device)
+            op = _flat(q_out, _BF16, "q_out", index, (n, h, d))
+        _check(_lib().mxq_kv_append(qp, k.data_ptr(), v.data_ptr(), k.dtype is _BF16, op, pp, ctypes.byref(r), cache._ref,
+                                    ctypes.byref(s), n, h, qs, ks, vs, _raw_stream(index, stream)), "mxq_kv_append")
     return q_out
 
 
 def paged_attn_workspace(cache, block_table, cu_q, kv_lens, tokens, heads, max_q):
     """Bytes of workspace that paged_attn uses for these sizes."""
-    s = _seqs_of(cache, block_table, cu_q, kv_lens)
-    return _lib().mxq_paged_attn_workspace(ctypes.byref(cache._c), ctypes.byref(s), tokens, heads, max_q)
+    s = _seqs_of(cache._index, block_table, cu_q, kv_lens)
+    return _lib().mxq_paged_attn_workspace(cache._ref, ctypes.byref(s), tokens, heads, max_q)
 
 
 def paged_attn(q, cache, block_table, cu_q, kv_lens, scale=None, window=0, max_q=None, out=None, lse=None,
@@ -279,33 +305,33 @@ def paged_attn(q, cache, block_table, cu_q, kv_lens, scale=None, window=0, max_q
     tokens) is a hint, the largest number of new tokens of a sequence; lse: float32 [tokens, heads] to receive
     the log-sum-exp; workspace: uint8, at least paged_attn_workspace bytes (allocated when None).  Rows outside
     every sequence are left as they were (in an `out` allocated here: uninitialised)."""
-    qs = _heads_of(q, _BF16, "q", cache.device)
-    dev = cache.device
+    index = cache._index
+    qs = _heads_of(q, (_BF16,), "q", index)
     n, h, d = q.shape
-    if d != cache.shape[3]:
-        raise ValueError(f"q {tuple(q.shape)} and the cache {cache.shape} disagree")
-    s = _seqs_of(cache, block_table, cu_q, kv_lens)
+    if d != cache._c.head_dim:
+        raise ValueError(f"q {tuple(q.shape)} and the cache {tuple(cache.shape)} disagree")
+    s = _seqs_of(index, block_table, cu_q, kv_lens)
     if scale is None:
         scale = 1.0 / math.sqrt(d) if d else 1.0
     if max_q is None:
         max_q = n
     L = _lib()
-    c, sp = ctypes.byref(cache._c), ctypes.byref(s)
-    if lse is not None:
-        _flat(lse, _F32, "lse", dev, (n, h))
-    with _on(dev, stream):
+    sp = ctypes.byref(s)
+    lp = None if lse is None else _flat(lse, _F32, "lse", index, (n, h))
+    wp, size = None, 0
+    with _on(index, stream):
         if out is None:
-            out = torch.empty((n, h, d), dtype=torch.bfloat16, device=dev)
-        else:
-            _flat(out, _BF16, "out", dev, (n, h, d))
+            out = torch.empty((n, h, d), dtype=_BF16, device=cache.device)
+        op = _flat(out, _BF16, "out", index, (n, h, d))
         if workspace is None:
-            need = L.mxq_paged_attn_workspace(c, sp, n, h, max_q)
-            if need > 0:
-                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+            size = L.mxq_paged_attn_workspace(cache._ref, sp, n, h, max_q)
+            if size > 0:
+                workspace = torch.empty((size,), dtype=_U8, device=cache.device)
+                wp = workspace.data_ptr()
+            size = max(size, 0)
         else:
-            _flat(workspace, _U8, "workspace", dev)
-        _check(L.mxq_paged_attn(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), c, sp, n, h,
-                                qs, scale, window, max_q, None if workspace is None else workspace.data_ptr(),
-                                0 if workspace is None else workspace.numel(), _raw_stream(dev, stream)),
-               "mxq_paged_attn")
+            size = workspace.numel() if isinstance(workspace, _Tensor) else 0
+            wp = _flat(workspace, _U8, "workspace", index, (size,))
+        _check(L.mxq_paged_attn(q.data_ptr(), op, lp, cache._ref, sp, n, h, qs, scale, window, max_q, wp, size,
+                                _raw_stream(index, stream)), "mxq_paged_attn")
     return out
