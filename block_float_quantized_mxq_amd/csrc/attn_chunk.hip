@@ -48,10 +48,10 @@ struct Tile {
     }
 };
 
-// How the 256 threads share the loads of a tile's rows (one half, k or v).
-template <int D, int FMT>
+// How the threads share the loads of a tile's rows (one half, k or v).
+template <int D, int FMT, int NW>
 struct Stage {
-    static constexpr int NT = 256;
+    static constexpr int NT = 64 * NW;
     static constexpr int VEC = FMT == kKvBf16 ? 8 : 16;       // elements per 16-byte load
     static constexpr int TPR = D / VEC;                       // threads per row
     static constexpr int RPP = NT / TPR;                      // rows per pass
@@ -59,16 +59,17 @@ struct Stage {
     static constexpr int RPW = 64 / TPR;                      // rows per wave and pass
 };
 
-template <int D, int FMT>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnArgs a, AttnPlan plan) {
+template <int D, int FMT, int NW>
+__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnArgs a, AttnPlan plan) {
     using T = Tile<D>;
-    using St = Stage<D, FMT>;
+    using St = Stage<D, FMT, NW>;
+    constexpr int ROWS = 32 * NW;
     constexpr int NB = kKeyBlocks<D>, kKeys = T::kKeys;
     constexpr int KSTEPS = D / 16;  // MFMA steps of the first product
     constexpr int DB = D / 32;      // 32-row blocks of O^T
     __shared__ __attribute__((aligned(16))) uint8_t k_lds[2][T::kBytes];
     __shared__ __attribute__((aligned(16))) uint8_t v_lds[2][T::kBytes];
-    __shared__ int taken_out;  // whether a value that is not finite was staged as zero
+    __shared__ int taken_out, bad_pages;  // whether a value that is not finite was staged as zero
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid / 64);
     const int half = lane >> 5, col = lane & 31;
@@ -76,7 +77,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
     // the last tiles of a sequence see the most keys: they start first
     const int index = (int)(gridDim.x / (unsigned)a.cache.heads) - 1 - (int)(blockIdx.x / (unsigned)a.cache.heads);
     int sid, tile;
-    if (!find_tile<kChunkRows, false>(a, plan, index, &sid, &tile)) return;
+    if (!find_tile<ROWS, false>(a, plan, index, &sid, &tile)) return;
     const Seq seq = sequence(a.seqs, a.tokens, sid);
     const Span span = span_of(a, plan, seq);
     int shares;
@@ -85,7 +86,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
     if (z > 0 && z >= shares) return;
 
     const int g = plan.group, rows = seq.n * g;
-    const int first = tile * kChunkRows, last = (first + kChunkRows < rows ? first + kChunkRows : rows) - 1;
+    const int first = tile * ROWS, last = (first + ROWS < rows ? first + ROWS : rows) - 1;
     const int cap = (int)((int64_t)a.seqs.max_pages << a.cache.page_shift);
     // positions that all rows of the tile see: [lo_in, hi_in); that some see: [lo_out, hi_out)
     int lo_out, hi_in, lo_in, hi_out;
@@ -128,17 +129,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
 
     const int ps = a.cache.page_shift, pmask = (1 << ps) - 1;
     const int32_t* table = a.seqs.table + sid * a.seqs.table_stride;
-    // page ids of the 16-key groups of a tile; a group's rows lie in one page
-    typedef int Ids __attribute__((ext_vector_type(4)));
+    // A wave's rows of a pass lie in one group of 16 positions, and so in one
+    // page: its id, and the first row's address in units of rows.
+    typedef int Ids __attribute__((ext_vector_type(8)));
+    auto page_at = [&](int k) __attribute__((always_inline)) {
+        const int p = k >> ps;
+        return table[p < a.seqs.max_pages ? p : a.seqs.max_pages - 1];
+    };
     auto pages_of = [&](int k0) __attribute__((always_inline)) {
-        Ids id = {0, 0, 0, 0};
+        Ids id = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 2 * NB; ++i) {
-            const int p = (k0 + 16 * i) >> ps;
-            id[i] = table[p < a.seqs.max_pages ? p : a.seqs.max_pages - 1];
-        }
+        for (int n = 0; n < St::PASSES; ++n) id[n] = page_at(k0 + n * St::RPP + wave * St::RPW);
         return id;
     };
+    bool some_bad = false;
     const int srow = lane / St::TPR, schunk = lane % St::TPR;
     // what this thread carries of the next tile
     u32x4_t kst[St::PASSES], vst[St::PASSES];
@@ -151,11 +155,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
 #pragma unroll
         for (int n = 0; n < St::PASSES; ++n) {
             const int row0 = n * St::RPP + wave * St::RPW;  // of this wave and pass; one 16-key group
-            int page = id[0];
-            if (row0 >= 16) page = id[1];
-            if (row0 >= 32) page = id[2];
-            if (row0 >= 48) page = id[3];
-            if (page < 0 || page >= a.cache.pages) page = 0;
+            const int page = ((id[n] < 0) | (id[n] >= a.cache.pages)) ? 0 : id[n];
             const int64_t base = (((int64_t)page * a.cache.heads + kvh) << ps) + ((k0 + row0) & pmask);
             const uint32_t off = (uint32_t)(srow * D * (int)EB + schunk * 16);
             x[n] = *reinterpret_cast<const u32x4_t*>(static_cast<const uint8_t*>(half_base) + base * D * EB + off);
@@ -166,12 +166,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
         load(a.cache.k, a.cache.ks, k0, id, kst, ksc);
         load(a.cache.v, a.cache.vs, k0, id, vst, vsc);
     };
-    // Groups of a tile whose page is out of range, as bits.
-    auto bad_groups = [&](int k0, const Ids id) __attribute__((always_inline)) {
+    // The 16-position groups of a tile whose page is out of range, as bits;
+    // bad_pages says whether there are any at all.
+    auto bad_groups = [&](int k0) __attribute__((always_inline)) {
         int bad = 0;
+        if (some_bad) {
 #pragma unroll
-        for (int i = 0; i < 2 * NB; ++i)
-            if (k0 + 16 * i < end && (id[i] < 0 || id[i] >= a.cache.pages)) bad |= 1 << i;
+            for (int i = 0; i < 4; ++i) {
+                const int page = page_at(k0 + 16 * i);
+                if (k0 + 16 * i < end && (page < 0 || page >= a.cache.pages)) bad |= 1 << i;
+            }
+        }
         return bad;
     };
     auto masked_tile = [&](int k0, int bad) __attribute__((always_inline)) { return k0 + kKeys > hi_in || k0 < lo_in || k0 + kKeys > end || bad != 0; };
@@ -224,12 +229,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
     };
 
     if (t0 < end) {
-        if (tid == 0) taken_out = 0;
+        if (tid == 0) taken_out = bad_pages = 0;
+        __syncthreads();
+        for (int p = (t0 >> ps) + tid; p <= (end - 1) >> ps; p += 64 * NW) {
+            const int page = table[p];
+            if (page < 0 || page >= a.cache.pages) bad_pages = 1;
+        }
         const Ids id = pages_of(t0);
         load_tile(t0, id);
         Ids id_next = pages_of(t0 + kKeys);
-        int bad = bad_groups(t0, id);
         __syncthreads();
+        some_bad = __builtin_amdgcn_readfirstlane(bad_pages) != 0;
+        int bad = bad_groups(t0);
         store_k(0);
         store_v(t0, 0, bad);
         __syncthreads();
@@ -239,18 +250,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
             int bad_next = 0;
             if (more) {
                 load_tile(k0 + kKeys, id_next);
-                bad_next = bad_groups(k0 + kKeys, id_next);
+                bad_next = bad_groups(k0 + kKeys);
                 id_next = pages_of(k0 + 2 * kKeys);
             }
             // ---- scores ----
             const uint8_t* kt = k_lds[number & 1];
             f32x16 s[NB];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[b][i] = 0.0f;
 #pragma unroll
-                for (int t = 0; t < KSTEPS; ++t) {
+            for (int t = 0; t < KSTEPS; ++t) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
                     const u32x4_t w = *reinterpret_cast<const u32x4_t*>(
                         kt + (b * 32 + col) * (D * 2) + 16 * T::k_chunk(col, 2 * t + half));
                     s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), q[t], s[b], 0, 0, 0);
@@ -320,8 +333,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
         if (taken_out) {
 #pragma unroll 1
             for (int k0 = t0; k0 < end; k0 += kKeys) {
-                const Ids ids = pages_of(k0);
-                if (!masked_tile(k0, bad_groups(k0, ids))) continue;
+                if (!masked_tile(k0, bad_groups(k0))) continue;
 #pragma unroll 1
                 for (int key = k0; key < k0 + kKeys && key < end; ++key) {
                     const int64_t page = table[key >> ps];
@@ -374,19 +386,22 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnA
     }
 }
 
-template <int D>
+template <int D, int NW>
 static void launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-    const int64_t tiles = a.tokens * p.group / kChunkRows + a.seqs.seqs;
-    const dim3 grid((unsigned)(tiles * a.cache.heads), (unsigned)p.splits), block(256);
-    if (a.cache.fmt == kKvMxfp8) hipLaunchKernelGGL((attn_chunk_kernel<D, kKvMxfp8>), grid, block, 0, st, a, p);
-    else hipLaunchKernelGGL((attn_chunk_kernel<D, kKvBf16>), grid, block, 0, st, a, p);
+    const int64_t tiles = a.tokens * p.group / (32 * NW) + a.seqs.seqs;
+    const dim3 grid((unsigned)(tiles * a.cache.heads), (unsigned)p.splits), block(64 * NW);
+    if (a.cache.fmt == kKvMxfp8) hipLaunchKernelGGL((attn_chunk_kernel<D, kKvMxfp8, NW>), grid, block, 0, st, a, p);
+    else hipLaunchKernelGGL((attn_chunk_kernel<D, kKvBf16, NW>), grid, block, 0, st, a, p);
 }
 
 bool launch_attn_chunk(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
     switch (a.cache.dim) {
-        case 64: launch_dim<64>(a, p, st); return true;
-        case 128: launch_dim<128>(a, p, st); return true;
-        case 256: launch_dim<256>(a, p, st); return true;
+        case 64: launch_dim<64, 4>(a, p, st); return true;
+        case 128:
+            if (p.waves == 8) launch_dim<128, 8>(a, p, st);
+            else launch_dim<128, 4>(a, p, st);
+            return true;
+        case 256: launch_dim<256, 4>(a, p, st); return true;
     }
     return false;
 }

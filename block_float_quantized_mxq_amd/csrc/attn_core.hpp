@@ -27,7 +27,8 @@ struct AttnPlan {
     float c;        // |scale| * log2 e: scores are kept in powers of two
     int q_sign;     // -1, 0, 1: the sign of scale, applied to the queries
     int splits;     // chunk kernel: shares of the keys of a sequence, at most
-    int target;     // decode kernel: workgroups to split the work of a call into, about
+    int waves;      // chunk kernel: waves of a workgroup, 32 rows each
+    int target;     // decode kernel: workgroups to split the work of a call into, about; 0: no split
     int least;      // positions of a share, at least; a multiple of kSplitUnit
     int filter;     // 1: this kernel takes only the sequences on its side of kFewRows
     float* part_o;  // unnormalised sums of the shares: chunk [splits][tokens * heads][dim], decode [slot][16][dim]
@@ -57,6 +58,44 @@ template <bool FEW>
 __device__ __forceinline__ int rows_taken(const AttnPlan& p, int n) {
     const int rows = n * p.group;
     return (p.filter && (rows <= kFewRows) != FEW) ? 0 : rows;
+}
+
+// Maximum and sum over the two halves of a wave (lane l and l + 32), and over
+// pairs of 16-lane rows (l and l ^ 16); every lane ends with the result, in a
+// fixed order of operands.  (A vector's element goes through a variable before
+// it is bit-cast: the compiler takes element 0 otherwise.)
+__device__ __forceinline__ float max_halves(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ __forceinline__ float sum_halves(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+__device__ __forceinline__ float max_rows16(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
+}
+__device__ __forceinline__ float sum_rows16(float v) {
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    const uint32_t x = r[0], y = r[1];
+    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
+}
+
+// Maximum over the lanes of a wave.
+__device__ __forceinline__ float wave_max(float v) {
+    v = __builtin_fmaxf(v, dpp_f32<kDppQuadXor1>(v));
+    v = __builtin_fmaxf(v, dpp_f32<kDppQuadXor2>(v));
+    v = __builtin_fmaxf(v, dpp_f32<kDppRowHalfMirror>(v));
+    v = __builtin_fmaxf(v, dpp_f32<kDppRowMirror>(v));
+    return max_halves(max_rows16(v));
 }
 
 // Inclusive sum over the lanes of a wave.
@@ -126,7 +165,11 @@ __device__ __forceinline__ int share_of(const AttnPlan& p, const Span& s, int* s
 // plan.target (but plan.least at least), so that workgroups carry equal work
 // whatever the lengths are.  A call has at most plan.target / kv_heads + tiles
 // shares; those of tiles that are split (at most 2 plan.target / kv_heads) have
-// a slot each for their partial result.
+// a slot each for their partial result.  Where the tiles alone fill the device
+// and no length is far above the mean, nothing is split: 32 sequences of 8000
+// positions, 40/8 heads of 128 in bf16, take 157 us whole and 171 us in 2304
+// shares; 64 sequences of 165 to 16000 positions (MXFP8) 258 us whole and 207.
+constexpr int kEnoughTiles = 256;
 struct Work {
     int sid, tile, z;     // sequence, tile of it, share of the tile
     int shares, share;    // of the tile; their length
@@ -148,15 +191,19 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, const AttnPlan& p, 
     };
     int tiles0, units0;  // the first 64 sequences' stay in registers
     load(0, &tiles0, &units0);
-    float total = 0.0f;
+    float total = 0.0f, count = 0.0f, longest = 0.0f;
     for (int base = 0; base < a.seqs.seqs; base += 64) {
         int tiles = tiles0, units = units0;
         if (base) load(base, &tiles, &units);
         total += group_sum<64>((float)tiles * (float)units);
+        count += group_sum<64>((float)tiles);
+        longest = __builtin_fmaxf(longest, wave_max(tiles ? (float)units : 0.0f));
     }
-    int per = __builtin_amdgcn_readfirstlane(
-        (int)__builtin_fminf(__builtin_ceilf(total * (float)a.cache.heads / (float)p.target), 16777216.0f));
-    if (per < p.least / kSplitUnit) per = p.least / kSplitUnit;
+    const float heads = (float)a.cache.heads;
+    float want = longest;
+    if (p.target > 0 && (count * heads < kEnoughTiles || longest * count > 1.25f * total))
+        want = __builtin_fmaxf(__builtin_ceilf(total * heads / (float)p.target), (float)(p.least / kSplitUnit));
+    const int per = __builtin_amdgcn_readfirstlane((int)__builtin_fminf(__builtin_fmaxf(want, 1.0f), 16777216.0f));
     int before = 0, slots = 0;
     for (int base = 0; base < a.seqs.seqs; base += 64) {
         int tiles = tiles0, units = units0;
@@ -192,35 +239,6 @@ __device__ __forceinline__ void seen_by(const AttnArgs& a, int64_t p, int cap, i
 }
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
-
-// Maximum and sum over the two halves of a wave (lane l and l + 32), and over
-// pairs of 16-lane rows (l and l ^ 16); every lane ends with the result, in a
-// fixed order of operands.  (A vector's element goes through a variable before
-// it is bit-cast: the compiler takes element 0 otherwise.)
-__device__ __forceinline__ float max_halves(float v) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, v);
-    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-    const uint32_t x = r[0], y = r[1];
-    return __builtin_fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
-}
-__device__ __forceinline__ float sum_halves(float v) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, v);
-    const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-    const uint32_t x = r[0], y = r[1];
-    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
-}
-__device__ __forceinline__ float max_rows16(float v) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, v);
-    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-    const uint32_t x = r[0], y = r[1];
-    return __builtin_fmaxf(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y));
-}
-__device__ __forceinline__ float sum_rows16(float v) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, v);
-    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-    const uint32_t x = r[0], y = r[1];
-    return __builtin_bit_cast(float, x) + __builtin_bit_cast(float, y);
-}
 
 // 4 bf16 of a column of a row-major LDS tile: each 16-lane group reads a
 // 4 x 16 block (lane l its elements 4 (l % 4) .. of row l / 4) and lane l gets
@@ -285,7 +303,5 @@ inline int64_t decode_shares(const AttnArgs& a, const AttnPlan& p) {
 bool launch_attn_chunk(const AttnArgs& a, const AttnPlan& p, hipStream_t st);
 bool launch_attn_decode(const AttnArgs& a, const AttnPlan& p, hipStream_t st);
 
-// Rows per workgroup of the chunk kernel; the decode kernel's is kFewRows.
-constexpr int kChunkRows = 128;
 
 }  // namespace mxq

@@ -166,46 +166,80 @@ namespace {
 
 struct Choice {
     bool few, many;
-    int target;       // workgroups of the decode kernel
-    int many_splits;  // shares of a sequence of the chunk kernel
+    int target;  // decode kernel: shares of the call
+    int waves;   // chunk kernel: waves of a workgroup
+    int splits;  // chunk kernel: shares of a sequence
 };
+
+// The chunk kernel's workgroups and shares, from what one 64-key tile takes (a
+// model of MI355X measurements, in microseconds).  Heads of 128: two
+// workgroups of 4 waves on a compute unit take 2.18 a tile together, one alone
+// 1.64; one of 8 waves takes 1.95 for its 256 rows.  (512 tokens over 16k,
+// 40/8 heads: 4 waves x 3 shares 220 us, 8 waves x 3 shares 199, unsplit 420;
+// a 1000-token prompt: 4 waves unsplit 38 us, 8 waves 42, 3 shares 55.)  Heads
+// of 256 run one workgroup at a time, heads of 64 like those of 128 at about
+// half the time.  Shares cost their partial sums, written and read, and a launch.
+void choose_chunk(Choice* c, int64_t rows_head, int64_t kv_heads, int64_t dim, double tiles) {
+    double best = 1e30;
+    for (int waves = 4; waves <= (dim == 128 ? 8 : 4); waves += 4) {
+        const double pair = dim == 256 ? 9.0 : dim == 64 ? 1.2 : 2.18, alone = dim == 256 ? 4.5 : dim == 64 ? 0.9 : 1.64;
+        const int64_t units = ((rows_head + 32 * waves - 1) / (32 * waves)) * kv_heads;
+        for (int64_t s = 1; s <= kMaxSplits && (s == 1 || 64.0 * tiles >= 256.0 * (double)s); ++s) {
+            const int64_t n = units * s;
+            double t;
+            if (waves == 8) {
+                t = 1.95 * (double)((n + kDesignCus - 1) / kDesignCus);
+            } else {
+                const int64_t rest = n % (2 * kDesignCus);
+                t = pair * (double)(n / (2 * kDesignCus)) + (rest > kDesignCus ? pair : rest > 0 ? alone : 0.0);
+            }
+            t *= tiles / (double)s;
+            if (s > 1) t += 8.0 + (double)(rows_head * kv_heads * dim * 8 * s) / 4e6;
+            if (t < best) {
+                best = t;
+                c->waves = waves;
+                c->splits = (int)s;
+            }
+        }
+    }
+}
 
 // Which kernels run, and into how many shares the positions are split.  max_q
 // is a hint: if it puts every sequence's rows below kFewRows the decode kernel
 // takes all; else the chunk kernel runs, and beside it the decode kernel if the
 // number of tokens leaves room for sequences with few.
-Choice choose(int64_t group, int64_t kv_heads, int64_t tokens, int64_t seqs, int64_t positions, int64_t max_q) {
+Choice choose(int64_t group, int64_t kv_heads, int64_t dim, int64_t tokens, int64_t seqs, int64_t positions, int64_t max_q) {
     const int64_t most_q = max_q < tokens ? max_q : tokens;
     Choice c{};
     c.many = most_q * group > kFewRows;
     c.few = !c.many || (seqs > 1 && 4 * tokens < 3 * seqs * most_q);
-    // Few tiles: three workgroups are resident on a compute unit, one round of
-    // them; more tiles have other lengths each: more and shorter shares even
-    // out the last round.
-    c.target = (seqs * kv_heads <= 64 ? 3 : 9) * kDesignCus;
-    c.many_splits = 1;
+    if (c.few) {
+        // Few tiles: about as many shares as workgroups are resident less one
+        // a compute unit; more tiles have other lengths each, and more and
+        // shorter shares even out the last round.  (Heads of 128: one token
+        // over 131071 51 us in 512 shares, 64 in 2304.)
+        const int64_t units = (c.many ? seqs : tokens * group / kFewRows + seqs) * kv_heads;
+        c.target = units > 64 ? 9 * kDesignCus : (dim == 64 ? 3 : dim == 128 ? 2 : 1) * kDesignCus;
+        // Short tables: the join's launch costs more than the split saves (one
+        // token over 500 positions 14.8 us whole and 19.3 split, over 1000 17.1
+        // and 20.1; 8 sequences of 900 20.2 and 20.7; calls included).
+        if (positions <= 1024) c.target = 0;
+    }
+    c.waves = 4;
+    c.splits = 1;
     if (c.many) {
-        // two workgroups are resident on a compute unit: the number of shares
-        // that fills the last round best, with a price for each share's join
-        const int64_t units = ((tokens * group + kChunkRows - 1) / kChunkRows) * kv_heads;
-        const int64_t top = (positions + 255) / 256;
-        double best = 1e30;
-        for (int64_t s = 1; s <= kMaxSplits && s <= top; ++s) {
-            const double rounds = (double)((units * s + 2 * kDesignCus - 1) / (2 * kDesignCus));
-            const double cost = rounds / (double)s * (1.0 + 0.03 * (double)(s - 1));
-            if (cost < best) {
-                best = cost;
-                c.many_splits = (int)s;
-            }
-        }
+        const double seen = (double)positions - 0.5 * (double)(most_q < positions ? most_q : positions);
+        choose_chunk(&c, tokens * group, kv_heads, dim, seen < 64.0 ? 1.0 : seen / 64.0);
     }
     return c;
 }
 
 // Rows of the partial results.  Decode: a split tile has less than twice its
 // part of the target in shares, and a slot each.
-int64_t chunk_rows(const Choice& c, int64_t rows) { return c.many && c.many_splits > 1 ? c.many_splits * rows : 0; }
-int64_t decode_rows(const Choice& c, int64_t kv_heads) { return c.few ? (2 * (c.target / kv_heads) + 2) * kv_heads * kFewRows : 0; }
+int64_t chunk_rows(const Choice& c, int64_t rows) { return c.many && c.splits > 1 ? c.splits * rows : 0; }
+int64_t decode_rows(const Choice& c, int64_t kv_heads) {
+    return c.few && c.target > 0 ? (2 * (c.target / kv_heads) + 2) * kv_heads * kFewRows : 0;
+}
 
 AttnPlan plan_of(const AttnArgs& a, bool filter, int64_t rows, float* ws) {
     AttnPlan p{};
@@ -214,7 +248,7 @@ AttnPlan plan_of(const AttnArgs& a, bool filter, int64_t rows, float* ws) {
     p.c = mag == 0.0f ? 1.0f : mag * 1.44269504088896341f;
     p.q_sign = a.scale > 0.0f ? 1 : a.scale < 0.0f ? -1 : 0;
     p.splits = 1;
-    p.target = 1;
+    p.waves = 4;
     p.filter = filter ? 1 : 0;
     p.part_o = ws;
     p.part_m = ws + rows * a.cache.dim;
@@ -226,20 +260,20 @@ AttnPlan plan_of(const AttnArgs& a, bool filter, int64_t rows, float* ws) {
 
 int64_t paged_attn_workspace(int64_t heads, int64_t kv_heads, int64_t dim, int64_t tokens, int64_t seqs,
                              int64_t max_pages, int64_t page_size, int64_t max_q) {
-    const Choice c = choose(heads / kv_heads, kv_heads, tokens, seqs, max_pages * page_size, max_q);
+    const Choice c = choose(heads / kv_heads, kv_heads, dim, tokens, seqs, max_pages * page_size, max_q);
     return 4 * (dim + 2) * (chunk_rows(c, tokens * heads) + decode_rows(c, kv_heads));
 }
 
 bool launch_paged_attn(const AttnArgs& a, hipStream_t st) {
-    const Choice c = choose(a.heads / a.cache.heads, a.cache.heads, a.tokens, a.seqs.seqs,
+    const Choice c = choose(a.heads / a.cache.heads, a.cache.heads, a.cache.dim, a.tokens, a.seqs.seqs,
                             (int64_t)a.seqs.max_pages << a.cache.page_shift, a.max_q);
     float* ws = static_cast<float*>(a.workspace);
     if (c.few) {
         AttnPlan p = plan_of(a, c.many, decode_rows(c, a.cache.heads), ws);
         p.target = c.target;
-        p.least = 128;
+        p.least = decode_tiles(a, p) * a.cache.heads < kEnoughTiles ? 128 : 512;
         if (!launch_attn_decode(a, p, st)) return false;
-        switch (a.cache.dim) {
+        if (c.target > 0) switch (a.cache.dim) {
             case 64: launch_join_decode<64>(a, p, st); break;
             case 128: launch_join_decode<128>(a, p, st); break;
             case 256: launch_join_decode<256>(a, p, st); break;
@@ -248,10 +282,11 @@ bool launch_paged_attn(const AttnArgs& a, hipStream_t st) {
     }
     if (c.many) {
         AttnPlan p = plan_of(a, c.few, chunk_rows(c, a.tokens * a.heads), ws);
-        p.splits = c.many_splits;
+        p.splits = c.splits;
+        p.waves = c.waves;
         p.least = 256;
         if (!launch_attn_chunk(a, p, st)) return false;
-        if (c.many_splits > 1) {
+        if (c.splits > 1) {
             switch (a.cache.dim) {
                 case 64: launch_join_chunk<64>(a, p, st); break;
                 case 128: launch_join_chunk<128>(a, p, st); break;
