@@ -16,6 +16,7 @@ constexpr int64_t kMaxTokens = int64_t(1) << 22;  // one workgroup a token: 2^30
 
 constexpr int64_t kMaxRows = int64_t(1) << 25;      // query rows: workgroups of every launch stay below 2^24
 constexpr int64_t kMaxPositions = int64_t(1) << 30;  // of a sequence
+constexpr float kMaxScale = 0x1p100f;                 // of the scores: scale * log2 e stays finite
 constexpr int64_t kMaxStride = int64_t(1) << 36;  // 2^22 tokens of 4 bytes: offsets stay within 64 bits
 constexpr int64_t kMaxRopeStride = int64_t(1) << 28;  // 2^31 tokens
 
@@ -193,7 +194,7 @@ MXQ_API mxq_status_t mxq_paged_attn(const uint16_t* q, uint16_t* out, float* lse
     if (!q || !out || !cache || !seqs || cache_null(*cache) || seqs_null(*seqs)) return MXQ_E_NULLPTR;
     if (!cache_shape_ok(*cache, *seqs, tokens, heads) || heads > kMaxInt || cache->head_dim > kMaxInt ||
         !stride_ok(q_stride, heads, cache->head_dim) || window < 0 || max_q <= 0 || workspace_bytes < 0 ||
-        !std::isfinite(scale))
+        !(std::fabs(scale) <= kMaxScale))
         return MXQ_E_SHAPE;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
         !cache_align_ok(*cache, *seqs) || !stride_aligned(q_stride, 2))

@@ -164,10 +164,11 @@ def _rope_params(inv_freq, layout, mscale, index):
 
 
 class KVCache:
-    """A paged cache over the caller's tensors: k, v [pages, kv_heads, page_size, head_dim] in bfloat16, or uint8
-    E4M3 codes with uint8 E8M0 scales k_scales, v_scales [pages, kv_heads, page_size, head_dim / 32]."""
+    """A paged cache over the caller's tensors, made once and kept: k, v [pages, kv_heads, page_size, head_dim] in
+    bfloat16, or uint8 E4M3 codes with uint8 E8M0 scales k_scales, v_scales [pages, kv_heads, page_size,
+    head_dim / 32]."""
 
-    __slots__ = ("k", "v", "k_scales", "v_scales", "device", "shape", "format", "_index", "_c", "_ref")
+    __slots__ = ("_tensors", "device", "shape", "format", "_index", "_c", "_ref", "__weakref__")
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
         mx = k_scales is not None or v_scales is not None
@@ -185,11 +186,17 @@ class KVCache:
             want = (pages, heads, page, dim // 32)
             ks = _flat(k_scales, _U8, "cache k_scales", index, want)
             vs = _flat(v_scales, _U8, "cache v_scales", index, want)
-        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self._tensors = (k, v, k_scales, v_scales)
         self.device, self.shape, self.format = k.device, shape, KV_MXFP8 if mx else KV_BF16
         self._index = index
         self._c = _Cache(self.format, 0, kp, vp, ks, vs, pages, page, heads, dim)
         self._ref = ctypes.byref(self._c)
+
+    # read-only: the addresses were taken when the cache was made
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scales = property(lambda self: self._tensors[2])
+    v_scales = property(lambda self: self._tensors[3])
 
 
 def kv_cache(pages, kv_heads, page_size, head_dim, fmt="bf16", device="cuda"):
@@ -285,7 +292,9 @@ def kv_append(k, v, cache, block_table, cu_q, kv_lens, q=None, inv_freq=None, la
         if q is not None:
             if q_out is None:
                 q_out = torch.empty((n, h, d), dtype=_BF16, device=cache.device)
-            op = _flat(q_out, _BF16, "q_out", index, (n, h, d))
+                op = q_out.data_ptr()
+            else:
+                op = _flat(q_out, _BF16, "q_out", index, (n, h, d))
         _check(_lib().mxq_kv_append(qp, k.data_ptr(), v.data_ptr(), k.dtype is _BF16, op, pp, ctypes.byref(r), cache._ref,
                                     ctypes.byref(s), n, h, qs, ks, vs, _raw_stream(index, stream)), "mxq_kv_append")
     return q_out
@@ -294,7 +303,10 @@ def kv_append(k, v, cache, block_table, cu_q, kv_lens, q=None, inv_freq=None, la
 def paged_attn_workspace(cache, block_table, cu_q, kv_lens, tokens, heads, max_q):
     """Bytes of workspace that paged_attn uses for these sizes."""
     s = _seqs_of(cache._index, block_table, cu_q, kv_lens)
-    return _lib().mxq_paged_attn_workspace(cache._ref, ctypes.byref(s), tokens, heads, max_q)
+    size = _lib().mxq_paged_attn_workspace(cache._ref, ctypes.byref(s), tokens, heads, max_q)
+    if size < 0:
+        raise ValueError(f"no paged_attn of {tokens} tokens and {heads} heads with max_q {max_q} over {tuple(cache.shape)}")
+    return size
 
 
 def paged_attn(q, cache, block_table, cu_q, kv_lens, scale=None, window=0, max_q=None, out=None, lse=None,
@@ -322,7 +334,9 @@ def paged_attn(q, cache, block_table, cu_q, kv_lens, scale=None, window=0, max_q
     with _on(index, stream):
         if out is None:
             out = torch.empty((n, h, d), dtype=_BF16, device=cache.device)
-        op = _flat(out, _BF16, "out", index, (n, h, d))
+            op = out.data_ptr()
+        else:
+            op = _flat(out, _BF16, "out", index, (n, h, d))
         if workspace is None:
             size = L.mxq_paged_attn_workspace(cache._ref, sp, n, h, max_q)
             if size > 0:

@@ -155,7 +155,9 @@ mxq_status_t mxq_kv_append(const void *q, const void *k, const void *v, mxq_out_
  *   j <= p,  and j > p - window if window > 0:
  *   out = sum_j softmax_j(scale * q . k_j) v_j
  *   lse = log sum_j exp(scale * q . k_j)
- * with fp32 scores, statistics and sums, one pass over the keys.  The softmax
+ * with fp32 scores, statistics and sums, one pass over the keys.  MXFP8 rows
+ * are decoded to bf16: exact from scale byte 3 on, and below that rounded to
+ * bf16's smallest subnormal steps; scale byte 255 is NaN.  The softmax
  * weights enter the value product as bf16 (long chunks) or as a pair of bf16
  * (few rows); both accumulate in fp32.
  *   q      bf16 [tokens][heads][head_dim], tokens q_stride elements apart
@@ -169,7 +171,7 @@ mxq_status_t mxq_kv_append(const void *q, const void *k, const void *v, mxq_out_
  *          reads there: no clearing, and calls on one stream may share it;
  *          calls that overlap in time may not.
  *   limits on heads (a multiple of kv_heads), pages, sequences and strides as
- *   in mxq_kv_append; scale finite
+ *   in mxq_kv_append; |scale| up to 2^100;  out must not overlap q
  * A row that sees no position (kv_lens[s] smaller than its new tokens) gets
  * zeros and lse -inf.  kv_lens is taken as at most max_pages * page_size.  A
  * row that sees a position whose page is outside [0, num_pages) gets NaN.

@@ -133,6 +133,39 @@ class Case:
         return out, mag, reach, lse
 
 
+def attention_on(c, device, scale, window=0):
+    """Case.attention with one masked product per sequence and key/value head, in 64 bits on the device."""
+    g = c.heads // c.kv_heads
+    out = torch.full((c.tokens, c.heads, c.dim), float("nan"), dtype=torch.float64, device=device)
+    mag, lse = out.clone(), out[..., 0].clone()
+    reach = lse.clone()
+    for s, (new, n) in enumerate(c.seqs):
+        if new == 0:
+            continue
+        t0 = int(c.cu[s])
+        p = torch.arange(n - new, n, device=device)[:, None]
+        for h in range(c.kv_heads):
+            k, v = c.cached("k", s, h).to(device), c.cached("v", s, h).to(device)
+            j = torch.arange(k.shape[0], device=device)[None]
+            seen = (j <= p) & (j > p - window if window else j >= 0)
+            for i in range(g):
+                q = c.q16[t0:t0 + new, h * g + i].to(device).double()
+                a = scale * (q @ k.t().contiguous())
+                a = torch.where(seen, a, -math.inf)
+                w = torch.softmax(a, -1)
+                # what a row does not see does not reach it, whatever it is
+                bad_v = ~v.isfinite().all(-1)
+                sl = (slice(t0, t0 + new), h * g + i)
+                clean = torch.where(bad_v[:, None], 0.0, v)
+                out[sl], mag[sl] = w @ clean, w @ clean.abs()
+                hit = (seen & bad_v[None]).any(-1)
+                out[sl] = torch.where(hit[:, None], float("nan"), out[sl])
+                kc = torch.nan_to_num(k, 0.0, 0.0, 0.0)
+                r = scale * torch.where(seen, q.abs() @ kc.abs().t().contiguous(), 0.0).amax(-1)
+                reach[sl], lse[sl] = r, torch.logsumexp(a, -1)
+    return tuple(t.cpu() for t in (out, mag, reach, lse))
+
+
 def turned(x, pos, inv_freq, layout, mscale):
     """(rotation of x [t, h, d] in 64 bits, |a| + |b| of each element's pair)."""
     x = x.double()

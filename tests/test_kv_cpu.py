@@ -129,7 +129,8 @@ def test_attention_refusals():
     for bad in (0, -1):
         for a in ("tokens", "heads", "pages", "page", "hk", "dim", "seqs", "width", "max_q"):
             assert attn(**{a: bad}) == SHAPE, a
-    assert attn(window=-1) == SHAPE and attn(scale=math.inf) == SHAPE and attn(scale=math.nan) == SHAPE
+    assert attn(window=-1) == SHAPE
+    assert attn(scale=math.inf) == SHAPE and attn(scale=math.nan) == SHAPE and attn(scale=-2.0 ** 101) == SHAPE
     assert attn(heads=5) == SHAPE and attn(page=48) == SHAPE and attn(qs=255) == SHAPE and attn(ws_bytes=-1) == SHAPE
     for a in ("q", "out", "ws", "ck", "cv"):
         assert attn(**{a: A + 8}) == ALIGN, a
