@@ -182,7 +182,7 @@ MXQ_API int64_t mxq_paged_attn_workspace(const mxq_kv_cache_t* cache, const mxq_
     if (!cache || !seqs || !cache_shape_ok(*cache, *seqs, tokens, heads) || max_q <= 0 ||
         !cache_supported(*cache, *seqs, tokens, heads))
         return -1;
-    return mxq::paged_attn_workspace(heads, cache->kv_heads, cache->head_dim, tokens, seqs->seqs, seqs->max_pages,
+    return mxq::paged_attn_workspace(heads, cache->kv_heads, cache->head_dim, cache->format == MXQ_KV_MXFP8, tokens, seqs->seqs, seqs->max_pages,
                                      cache->page_size, max_q);
 }
 

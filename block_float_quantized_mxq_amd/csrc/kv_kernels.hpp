@@ -81,7 +81,7 @@ bool launch_rope(const RopeArgs& a, hipStream_t st);
 bool launch_kv_append(const AppendArgs& a, hipStream_t st);
 bool launch_paged_attn(const AttnArgs& a, hipStream_t st);
 // Workspace of launch_paged_attn.
-int64_t paged_attn_workspace(int64_t heads, int64_t kv_heads, int64_t dim, int64_t tokens, int64_t seqs,
+int64_t paged_attn_workspace(int64_t heads, int64_t kv_heads, int64_t dim, bool mx, int64_t tokens, int64_t seqs,
                              int64_t max_pages, int64_t page_size, int64_t max_q);
 
 }  // namespace mxq

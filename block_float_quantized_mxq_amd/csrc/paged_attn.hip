@@ -172,29 +172,32 @@ struct Choice {
 };
 
 // The chunk kernel's workgroups and shares, from what one 64-key tile takes (a
-// model of MI355X measurements, in microseconds).  Heads of 128: two
-// workgroups of 4 waves on a compute unit take 2.18 a tile together, one alone
-// 1.64; one of 8 waves takes 1.95 for its 256 rows.  (512 tokens over 16k,
-// 40/8 heads: 4 waves x 3 shares 220 us, 8 waves x 3 shares 199, unsplit 420;
-// a 1000-token prompt: 4 waves unsplit 38 us, 8 waves 42, 3 shares 55.)  Heads
-// of 256 run one workgroup at a time, heads of 64 like those of 128 at about
-// half the time.  Shares cost their partial sums, written and read, and a launch.
-void choose_chunk(Choice* c, int64_t rows_head, int64_t kv_heads, int64_t dim, double tiles) {
+// model of MI355X measurements, in microseconds).  Heads of 128 in bf16: two
+// workgroups of 4 waves on a compute unit take 2.3 a tile together, one alone
+// 1.63; one of 8 waves takes 2.15 for its 256 rows, and longer to start.  (512
+// tokens over 16k, 40/8 heads: 4 waves x 3 shares 220 us, 8 waves x 3 shares
+// 199, unsplit 420; a 1000-token prompt: 4 waves unsplit 38 us, 8 waves 42, 3
+// shares 55.)  MXFP8 tiles take a sixth more.  Heads of 256 run one workgroup on
+// a compute unit, heads of 64 three.  Shares cost a launch and their partial
+// sums, half of which travel while others still compute.
+void choose_chunk(Choice* c, int64_t rows_head, int64_t kv_heads, int64_t dim, bool mx, double most, double mean) {
+    const double more = mx ? 1.16 : 1.0;
+    const double full = (dim == 256 ? 4.5 : dim == 64 ? 1.7 : 2.3) * more;  // of all that are resident together
+    const double two = (dim == 256 ? 4.5 : dim == 64 ? 1.25 : 2.3) * more, alone = (dim == 256 ? 4.5 : dim == 64 ? 0.85 : 1.63) * more;
+    const double eight = 2.15 * more;
+    const int64_t resident = (dim == 256 ? 1 : dim == 64 ? 3 : 2) * kDesignCus;
     double best = 1e30;
     for (int waves = 4; waves <= (dim == 128 ? 8 : 4); waves += 4) {
-        const double pair = dim == 256 ? 9.0 : dim == 64 ? 1.2 : 2.18, alone = dim == 256 ? 4.5 : dim == 64 ? 0.9 : 1.64;
         const int64_t units = ((rows_head + 32 * waves - 1) / (32 * waves)) * kv_heads;
-        for (int64_t s = 1; s <= kMaxSplits && (s == 1 || 64.0 * tiles >= 256.0 * (double)s); ++s) {
-            const int64_t n = units * s;
-            double t;
-            if (waves == 8) {
-                t = 1.95 * (double)((n + kDesignCus - 1) / kDesignCus);
-            } else {
-                const int64_t rest = n % (2 * kDesignCus);
-                t = pair * (double)(n / (2 * kDesignCus)) + (rest > kDesignCus ? pair : rest > 0 ? alone : 0.0);
-            }
-            t *= tiles / (double)s;
-            if (s > 1) t += 8.0 + (double)(rows_head * kv_heads * dim * 8 * s) / 4e6;
+        const int64_t slots = waves == 8 ? kDesignCus : resident;
+        for (int64_t s = 1; s <= kMaxSplits && (s == 1 || 64.0 * most >= 256.0 * (double)s); ++s) {
+            const int64_t n = units * s, rest = n % slots;
+            // the longest workgroup starts in the first round, the mean one in the others
+            double t = 0.0;
+            if (n >= slots) t = (waves == 8 ? eight : full) * (most + mean * (double)(n / slots - 1));
+            if (rest > 0) t += (waves == 8 ? eight : rest > kDesignCus ? two : alone) * (n < slots ? most : mean);
+            t = t / (double)s + (waves == 8 ? 6.0 : 3.0) * (double)((n + slots - 1) / slots);
+            if (s > 1) t += 8.0 + (double)(rows_head * kv_heads * dim * 4 * s) / 4e6;
             if (t < best) {
                 best = t;
                 c->waves = waves;
@@ -208,7 +211,8 @@ void choose_chunk(Choice* c, int64_t rows_head, int64_t kv_heads, int64_t dim, d
 // is a hint: if it puts every sequence's rows below kFewRows the decode kernel
 // takes all; else the chunk kernel runs, and beside it the decode kernel if the
 // number of tokens leaves room for sequences with few.
-Choice choose(int64_t group, int64_t kv_heads, int64_t dim, int64_t tokens, int64_t seqs, int64_t positions, int64_t max_q) {
+Choice choose(int64_t group, int64_t kv_heads, int64_t dim, bool mx, int64_t tokens, int64_t seqs, int64_t positions,
+              int64_t max_q) {
     const int64_t most_q = max_q < tokens ? max_q : tokens;
     Choice c{};
     c.many = most_q * group > kFewRows;
@@ -228,8 +232,9 @@ Choice choose(int64_t group, int64_t kv_heads, int64_t dim, int64_t tokens, int6
     c.waves = 4;
     c.splits = 1;
     if (c.many) {
-        const double seen = (double)positions - 0.5 * (double)(most_q < positions ? most_q : positions);
-        choose_chunk(&c, tokens * group, kv_heads, dim, seen < 64.0 ? 1.0 : seen / 64.0);
+        // tiles of the last row, and of a row on average
+        const double most = (double)(positions + 63) / 64.0;
+        choose_chunk(&c, tokens * group, kv_heads, dim, mx, most, most - (double)(most_q < positions ? most_q : positions) / 128.0);
     }
     return c;
 }
@@ -258,14 +263,14 @@ AttnPlan plan_of(const AttnArgs& a, bool filter, int64_t rows, float* ws) {
 
 }  // namespace
 
-int64_t paged_attn_workspace(int64_t heads, int64_t kv_heads, int64_t dim, int64_t tokens, int64_t seqs,
+int64_t paged_attn_workspace(int64_t heads, int64_t kv_heads, int64_t dim, bool mx, int64_t tokens, int64_t seqs,
                              int64_t max_pages, int64_t page_size, int64_t max_q) {
-    const Choice c = choose(heads / kv_heads, kv_heads, dim, tokens, seqs, max_pages * page_size, max_q);
+    const Choice c = choose(heads / kv_heads, kv_heads, dim, mx, tokens, seqs, max_pages * page_size, max_q);
     return 4 * (dim + 2) * (chunk_rows(c, tokens * heads) + decode_rows(c, kv_heads));
 }
 
 bool launch_paged_attn(const AttnArgs& a, hipStream_t st) {
-    const Choice c = choose(a.heads / a.cache.heads, a.cache.heads, a.cache.dim, a.tokens, a.seqs.seqs,
+    const Choice c = choose(a.heads / a.cache.heads, a.cache.heads, a.cache.dim, a.cache.fmt == kKvMxfp8, a.tokens, a.seqs.seqs,
                             (int64_t)a.seqs.max_pages << a.cache.page_shift, a.max_q);
     float* ws = static_cast<float*>(a.workspace);
     if (c.few) {
