@@ -29,6 +29,7 @@ struct AttnPlan {
     int splits;     // chunk kernel: shares of the keys of a sequence, at most
     int waves;      // chunk kernel: waves of a workgroup, 32 rows each
     int target;     // decode kernel: workgroups to split the work of a call into, about; 0: no split
+    int enough;     // decode kernel: tiles that fill the device unsplit
     int least;      // positions of a share, at least; a multiple of kSplitUnit
     int filter;     // 1: this kernel takes only the sequences on its side of kFewRows
     float* part_o;  // unnormalised sums of the shares: chunk [splits][tokens * heads][dim], decode [slot][16][dim]
@@ -169,7 +170,9 @@ __device__ __forceinline__ int share_of(const AttnPlan& p, const Span& s, int* s
 // and no length is far above the mean, nothing is split: 32 sequences of 8000
 // positions, 40/8 heads of 128 in bf16, take 157 us whole and 171 us in 2304
 // shares; 64 sequences of 165 to 16000 positions (MXFP8) 258 us whole and 207.
-constexpr int kEnoughTiles = 256;
+// A tile a compute unit fills it with heads of 128 in bf16; rows of fewer bytes
+// need two (the same 32 sequences in MXFP8: 124 us whole, 109 in shares; heads
+// of 64 in MXFP8: 88 and 61; 64 of those: 108 whole, 109 in shares).
 struct Work {
     int sid, tile, z;     // sequence, tile of it, share of the tile
     int shares, share;    // of the tile; their length
@@ -201,7 +204,7 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, const AttnPlan& p, 
     }
     const float heads = (float)a.cache.heads;
     float want = longest;
-    if (p.target > 0 && (count * heads < kEnoughTiles || longest * count > 1.25f * total))
+    if (p.target > 0 && (count * heads < (float)p.enough || longest * count > 1.25f * total))
         want = __builtin_fmaxf(__builtin_ceilf(total * heads / (float)p.target), (float)(p.least / kSplitUnit));
     const int per = __builtin_amdgcn_readfirstlane((int)__builtin_fminf(__builtin_fmaxf(want, 1.0f), 16777216.0f));
     int before = 0, slots = 0;

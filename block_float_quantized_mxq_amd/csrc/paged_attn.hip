@@ -276,7 +276,8 @@ bool launch_paged_attn(const AttnArgs& a, hipStream_t st) {
     if (c.few) {
         AttnPlan p = plan_of(a, c.many, decode_rows(c, a.cache.heads), ws);
         p.target = c.target;
-        p.least = decode_tiles(a, p) * a.cache.heads < kEnoughTiles ? 128 : 512;
+        p.enough = (a.cache.dim == 64 || a.cache.fmt == kKvMxfp8 ? 2 : 1) * kDesignCus;
+        p.least = decode_tiles(a, p) * a.cache.heads < kDesignCus ? 128 : 512;
         if (!launch_attn_decode(a, p, st)) return false;
         if (c.target > 0) switch (a.cache.dim) {
             case 64: launch_join_decode<64>(a, p, st); break;
