@@ -1,9 +1,9 @@
 // attn_chunk.hip -- paged attention for tiles of many query rows (a chunk of a
 // prompt, a whole prompt): matrix-core bound.
 //
-// A workgroup of 4 waves owns 128 rows (32 a wave) of one sequence and
-// key/value head and walks the keys they see in tiles of 64, staged in LDS as
-// bf16 and double buffered; the next tile's rows travel from HBM to registers
+// A workgroup of 4 or 8 waves owns 128 or 256 rows (32 a wave) of one sequence
+// and key/value head and walks the keys they see in tiles of 64, staged in LDS
+// as bf16 and double buffered; the next tile's rows travel from HBM to registers
 // while the current one is multiplied.
 //
 // Both products are taken transposed, S^T = K Q^T and O^T = V^T P^T, on the
@@ -22,16 +22,34 @@
 // The weights are rounded to bf16 for the second product: relative 2^-8 each,
 // of the same size as the rounding of the output, and averaged over the keys.
 // The softmax's sum takes the unrounded weights.
+//
+// Heads of 256 do not leave room for a row's queries and sums in the registers
+// of a wave that shares its SIMD: two waves share 32 rows, both take the whole
+// first product and each half of the output's elements.  That is half as much
+// matrix work again, and still faster than one wave a SIMD (a prompt of 4096
+// tokens, 16/2 heads: 229 us against 290).
+//
+// Measured (MI355X; bf16, 40/8 heads of 128): a prompt of 8192 tokens 705 us,
+// 975 TFLOP/s; 512 tokens over 16000 192 us with the join, 890 TFLOP/s.  A
+// library matrix product of 8192 x 8192 x 8192 takes 1390-1480 TFLOP/s, and a
+// loop of nothing but these MFMAs on such data 1756: the power limit, not the
+// issue rate, ends both.  Here the softmax's vector work and the staging share
+// the issue slots with the MFMAs: without any staging the same kernel took 26%
+// less, without the maximum 6%, without the page lookups 7%.
 #include "attn_core.hpp"
 
 namespace mxq {
 
 constexpr float kSlack = 8.0f;
 
-// Keys per tile, in blocks of the 32 of an MFMA: heads of 256 take half the keys, so that their sums and queries
-// still fit the registers of one wave.
+// Keys per tile, in blocks of the 32 of an MFMA: heads of 256 take half the keys (64 spill: 335 us against 331 for a
+// prompt of 4096 tokens split alike).
 template <int D>
 constexpr int kKeyBlocks = D == 256 ? 1 : 2;
+
+// Waves that share 32 rows, each with its part of the output's elements.
+template <int D>
+constexpr int kParts = D == 256 ? 2 : 1;
 
 // LDS tile of rows of D bf16, in 16-byte chunks; the chunk index is XORed
 // with bits of the row so that a column of rows (K: 16-byte reads of 32 rows)
@@ -60,13 +78,13 @@ struct Stage {
 };
 
 template <int D, int FMT, int NW>
-__global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_chunk_kernel(AttnArgs a, AttnPlan plan) {
+__global__ __launch_bounds__(64 * NW, 2) void attn_chunk_kernel(AttnArgs a, AttnPlan plan) {
     using T = Tile<D>;
     using St = Stage<D, FMT, NW>;
-    constexpr int ROWS = 32 * NW;
+    constexpr int PARTS = kParts<D>, ROWS = 32 * NW / PARTS;
     constexpr int NB = kKeyBlocks<D>, kKeys = T::kKeys;
     constexpr int KSTEPS = D / 16;  // MFMA steps of the first product
-    constexpr int DB = D / 32;      // 32-row blocks of O^T
+    constexpr int DB = D / 32 / PARTS;  // 32-row blocks of a wave's O^T
     __shared__ __attribute__((aligned(16))) uint8_t k_lds[2][T::kBytes];
     __shared__ __attribute__((aligned(16))) uint8_t v_lds[2][T::kBytes];
     __shared__ int taken_out, bad_pages;  // whether a value that is not finite was staged as zero
@@ -99,7 +117,8 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_chunk_kernel(A
     if (lo_out > t0) t0 = lo_out & ~(kKeys - 1);
 
     // this lane's row
-    const int r = first + wave * 32 + col;
+    const int part = wave / (NW / PARTS);  // of the elements
+    const int r = first + (wave - part * (NW / PARTS)) * 32 + col;
     const bool live = r < rows;
     const int tok = live ? r / g : 0, hg = live ? r - tok * g : 0;
     const int64_t token = seq.t0 + tok;
@@ -319,7 +338,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_chunk_kernel(A
             for (int t = 0; t < 2 * NB; ++t)
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
-                    const int off = 16 * ((4 * d + vchunk) ^ vx);
+                    const int off = 16 * ((4 * (DB * part + d) + vchunk) ^ vx);
                     const u32x2_t v0 = read_column4(vrow + (16 * t) * (D * 2) + off);
                     const u32x2_t v1 = read_column4(vrow + (16 * t + 8) * (D * 2) + off);
                     const u32x4_t v = {v0[0], v0[1], v1[0], v1[1]};
@@ -344,7 +363,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_chunk_kernel(A
                     for (int d = 0; d < DB; ++d)
 #pragma unroll
                         for (int i = 0; i < 16; i += 4) {
-                            const f32x4 x = not_finite_part<FMT>(a.cache.v, a.cache.vs, row, D, 32 * d + 2 * i + 4 * half, sees);
+                            const f32x4 x = not_finite_part<FMT>(a.cache.v, a.cache.vs, row, D, 32 * (DB * part + d) + 2 * i + 4 * half, sees);
 #pragma unroll
                             for (int j = 0; j < 4; ++j) o[d][i + j] += x[j];
                         }
@@ -360,18 +379,18 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_chunk_kernel(A
     if (shares <= 1) {
         const bool empty = hi <= lo;
         const float inv = empty ? 0.0f : 1.0f / l;
-        uint16_t* dst = a.out + at * D + 4 * half;
+        uint16_t* dst = a.out + at * D + 32 * DB * part + 4 * half;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
                 *reinterpret_cast<u32x2_t*>(dst + 32 * d + 2 * i) =
                     u32x2_t{pack_bf16(o[d][i] * inv, o[d][i + 1] * inv), pack_bf16(o[d][i + 2] * inv, o[d][i + 3] * inv)};
-        if (a.lse && half == 0)
+        if (a.lse && half == 0 && part == 0)
             a.lse[at] = empty ? -__builtin_inff() : (m + __builtin_amdgcn_logf(l)) * 0.69314718055994531f;
     } else {
         const int64_t slot = (int64_t)z * a.tokens * a.heads + at;
-        float* dst = plan.part_o + slot * D + 4 * half;
+        float* dst = plan.part_o + slot * D + 32 * DB * part + 4 * half;
         if (t0 < end) {
 #pragma unroll
             for (int d = 0; d < DB; ++d)
@@ -379,7 +398,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_chunk_kernel(A
                 for (int i = 0; i < 16; i += 4)
                     *reinterpret_cast<f32x4*>(dst + 32 * d + 2 * i) = f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
         }
-        if (half == 0) {
+        if (half == 0 && part == 0) {
             plan.part_m[slot] = m;
             plan.part_l[slot] = l;
         }
@@ -388,7 +407,7 @@ __global__ __launch_bounds__(64 * NW, D == 256 ? 1 : 2) void attn_chunk_kernel(A
 
 template <int D, int NW>
 static void launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
-    const int64_t tiles = a.tokens * p.group / (32 * NW) + a.seqs.seqs;
+    const int64_t tiles = a.tokens * p.group / (32 * NW / kParts<D>) + a.seqs.seqs;
     const dim3 grid((unsigned)(tiles * a.cache.heads), (unsigned)p.splits), block(64 * NW);
     if (a.cache.fmt == kKvMxfp8) hipLaunchKernelGGL((attn_chunk_kernel<D, kKvMxfp8, NW>), grid, block, 0, st, a, p);
     else hipLaunchKernelGGL((attn_chunk_kernel<D, kKvBf16, NW>), grid, block, 0, st, a, p);
@@ -401,7 +420,7 @@ bool launch_attn_chunk(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
             if (p.waves == 8) launch_dim<128, 8>(a, p, st);
             else launch_dim<128, 4>(a, p, st);
             return true;
-        case 256: launch_dim<256, 4>(a, p, st); return true;
+        case 256: launch_dim<256, 8>(a, p, st); return true;
     }
     return false;
 }

@@ -171,33 +171,43 @@ struct Choice {
     int splits;  // chunk kernel: shares of a sequence
 };
 
-// The chunk kernel's workgroups and shares, from what one 64-key tile takes (a
-// model of MI355X measurements, in microseconds).  Heads of 128 in bf16: two
-// workgroups of 4 waves on a compute unit take 2.3 a tile together, one alone
-// 1.63; one of 8 waves takes 2.15 for its 256 rows, and longer to start.  (512
-// tokens over 16k, 40/8 heads: 4 waves x 3 shares 220 us, 8 waves x 3 shares
-// 199, unsplit 420; a 1000-token prompt: 4 waves unsplit 38 us, 8 waves 42, 3
-// shares 55.)  MXFP8 tiles take a sixth more.  Heads of 256 run one workgroup on
-// a compute unit, heads of 64 three.  Shares cost a launch and their partial
-// sums, half of which travel while others still compute.
+// The chunk kernel's workgroups and shares, from a model of what they take (in
+// microseconds, fitted to MI355X measurements).  One 64-key tile, heads of 128
+// in bf16: two workgroups of 4 waves on a compute unit 2.3 together, one alone
+// 1.63; one of 8 waves 2.15 for its 256 rows, and longer to start.  (512 tokens
+// over 16k, 40/8 heads: 4 waves x 3 shares 220 us, 8 waves x 3 shares 195,
+// unsplit 420; a 1000-token prompt: 4 waves unsplit 37 us, 8 waves 41, 2 shares
+// 50.)  MXFP8 tiles take a sixth more.  Heads of 256 run one workgroup on a
+// compute unit, heads of 64 three.  Shares cost a launch and their partial sums
+// (a 4096-token prompt with 16/2 heads of 256: whole 229 us, 3 shares 326).
+//
+// most and mean: the tiles that the last row sees, and a row on average; rows
+// between see evenly fewer, so that some rows have nothing in the last shares.
 void choose_chunk(Choice* c, int64_t rows_head, int64_t kv_heads, int64_t dim, bool mx, double most, double mean) {
     const double more = mx ? 1.16 : 1.0;
-    const double full = (dim == 256 ? 4.5 : dim == 64 ? 1.7 : 2.3) * more;  // of all that are resident together
-    const double two = (dim == 256 ? 4.5 : dim == 64 ? 1.25 : 2.3) * more, alone = (dim == 256 ? 4.5 : dim == 64 ? 0.85 : 1.63) * more;
+    const double full = (dim == 256 ? 4.0 : dim == 64 ? 1.9 : 2.3) * more;  // of all that are resident together
+    const double two = (dim == 256 ? 4.0 : dim == 64 ? 1.25 : 2.3) * more, alone = (dim == 256 ? 4.0 : dim == 64 ? 0.85 : 1.63) * more;
     const double eight = 2.15 * more;
     const int64_t resident = (dim == 256 ? 1 : dim == 64 ? 3 : 2) * kDesignCus;
     double best = 1e30;
     for (int waves = 4; waves <= (dim == 128 ? 8 : 4); waves += 4) {
-        const int64_t units = ((rows_head + 32 * waves - 1) / (32 * waves)) * kv_heads;
-        const int64_t slots = waves == 8 ? kDesignCus : resident;
+        const double units = (double)(((rows_head + 32 * waves - 1) / (32 * waves)) * kv_heads);
+        const double slots = (double)(waves == 8 ? kDesignCus : resident), each = waves == 8 ? eight : full;
         for (int64_t s = 1; s <= kMaxSplits && (s == 1 || 64.0 * most >= 256.0 * (double)s); ++s) {
-            const int64_t n = units * s, rest = n % slots;
-            // the longest workgroup starts in the first round, the mean one in the others
-            double t = 0.0;
-            if (n >= slots) t = (waves == 8 ? eight : full) * (most + mean * (double)(n / slots - 1));
-            if (rest > 0) t += (waves == 8 ? eight : rest > kDesignCus ? two : alone) * (n < slots ? most : mean);
-            t = t / (double)s + (waves == 8 ? 6.0 : 3.0) * (double)((n + slots - 1) / slots);
-            if (s > 1) t += 8.0 + (double)(rows_head * kv_heads * dim * 4 * s) / 4e6;
+            // workgroups with something to do; their longest, mean and least work
+            const double n = s == 1 ? units : units * ((double)s * mean / most + (most - mean) / most);
+            const double long_s = most / (double)s, mean_s = units * mean / n, least_s = __builtin_fmax(2.0 * mean_s - long_s, 0.0);
+            const double whole = __builtin_floor(n / slots), rest = n - whole * slots;
+            // the longest start first, and the shortest even out the end
+            const double last = waves == 8 ? eight : rest > kDesignCus ? two : alone;
+            double t = last * long_s;
+            if (whole > 0.0) {
+                t = each * mean_s * whole;
+                if (rest > 0.0) t += last * (rest * mean_s + (slots - rest) * least_s) / slots;
+                t = __builtin_fmax(t, each * long_s);
+            }
+            t += (waves == 8 ? 6.0 : 3.0) * __builtin_ceil(n / slots);
+            if (s > 1) t += 12.0 + (double)(rows_head * kv_heads * dim * 4 * s) / 2.5e6;
             if (t < best) {
                 best = t;
                 c->waves = waves;
