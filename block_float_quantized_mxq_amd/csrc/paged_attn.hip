@@ -234,10 +234,12 @@ Choice choose(int64_t group, int64_t kv_heads, int64_t dim, bool mx, int64_t tok
         // over 131071 51 us in 512 shares, 64 in 2304.)
         const int64_t units = (c.many ? seqs : tokens * group / kFewRows + seqs) * kv_heads;
         c.target = units > 64 ? 9 * kDesignCus : (dim == 64 ? 3 : dim == 128 ? 2 : 1) * kDesignCus;
-        // Short tables: the join's launch costs more than the split saves (one
-        // token over 500 positions 14.8 us whole and 19.3 split, over 1000 17.1
-        // and 20.1; 8 sequences of 900 20.2 and 20.7; calls included).
-        if (positions <= 1024) c.target = 0;
+        // Short tables: the join's launch costs more than the split saves, in a
+        // captured graph below 500 positions of heads of 128, called one by one
+        // below 900 (one token over 1000: whole 15.7 us captured and 17.2
+        // called, split 11.0 and 18.2; 8 sequences of 600 called: 14.4 and
+        // 18.6; heads of 256, 2 of 600: 23.1 and 17.6).
+        if (positions * (dim == 64 ? 96 : dim) <= 768 * 128) c.target = 0;
     }
     c.waves = 4;
     c.splits = 1;
