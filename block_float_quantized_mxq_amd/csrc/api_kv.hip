@@ -12,12 +12,11 @@ namespace {
 using mxq::aligned;
 
 constexpr int64_t kMaxInt = (int64_t(1) << 31) - 1;
-constexpr int64_t kMaxTokens = int64_t(1) << 22;  // one workgroup a token: 2^30 work items
-
-constexpr int64_t kMaxRows = int64_t(1) << 25;      // query rows: workgroups of every launch stay below 2^24
-constexpr int64_t kMaxPositions = int64_t(1) << 30;  // of a sequence
+constexpr int64_t kMaxTokens = int64_t(1) << 22;      // one workgroup a token: 2^30 work items
+constexpr int64_t kMaxRows = int64_t(1) << 25;        // query rows: workgroups of every launch stay below 2^24
+constexpr int64_t kMaxPositions = int64_t(1) << 30;   // of a sequence
 constexpr float kMaxScale = 0x1p100f;                 // of the scores: scale * log2 e stays finite
-constexpr int64_t kMaxStride = int64_t(1) << 36;  // 2^22 tokens of 4 bytes: offsets stay within 64 bits
+constexpr int64_t kMaxStride = int64_t(1) << 36;      // 2^22 tokens of 4 bytes: offsets stay within 64 bits
 constexpr int64_t kMaxRopeStride = int64_t(1) << 28;  // 2^31 tokens
 
 int64_t elem_bytes(mxq_out_t t) { return t == MXQ_OUT_BF16 ? 2 : 4; }
@@ -52,10 +51,10 @@ bool cache_align_ok(const mxq_kv_cache_t& c, const mxq_kv_seqs_t& s) {
 }
 
 bool cache_supported(const mxq_kv_cache_t& c, const mxq_kv_seqs_t& s, int64_t tokens, int64_t heads) {
-    return tokens <= kMaxTokens && heads <= 65536 && tokens * heads <= kMaxRows &&
+    return tokens <= kMaxTokens && heads <= 65536 && tokens * heads <= kMaxRows && s.seqs <= MXQ_KV_MAX_SEQS &&
            s.seqs * c.kv_heads <= kMaxRows / 8 && c.num_pages <= kMaxInt && c.page_size >= 16 &&
            c.page_size <= MXQ_KV_MAX_PAGE && (c.head_dim == 64 || c.head_dim == 128 || c.head_dim == 256) &&
-           s.seqs <= MXQ_KV_MAX_SEQS && s.max_pages <= kMaxPositions / c.page_size && s.table_stride <= kMaxInt;
+           s.max_pages <= kMaxPositions / c.page_size && s.table_stride <= kMaxInt;
 }
 
 int log2_of(int64_t v) {
@@ -74,7 +73,7 @@ mxq::KvSeqs seqs_of(const mxq_kv_seqs_t& s) {
 }
 
 bool stride_ok(int64_t stride, int64_t heads, int64_t dim) { return stride >= heads * dim; }
-bool stride_aligned(int64_t stride, int64_t bytes) { return stride * bytes % 16 == 0; }
+bool stride_aligned(int64_t stride, int64_t bytes) { return stride % (16 / bytes) == 0; }
 
 }  // namespace
 
@@ -182,8 +181,8 @@ MXQ_API int64_t mxq_paged_attn_workspace(const mxq_kv_cache_t* cache, const mxq_
     if (!cache || !seqs || !cache_shape_ok(*cache, *seqs, tokens, heads) || max_q <= 0 ||
         !cache_supported(*cache, *seqs, tokens, heads))
         return -1;
-    return mxq::paged_attn_workspace(heads, cache->kv_heads, cache->head_dim, cache->format == MXQ_KV_MXFP8, tokens, seqs->seqs, seqs->max_pages,
-                                     cache->page_size, max_q);
+    return mxq::paged_attn_workspace(heads, cache->kv_heads, cache->head_dim, cache->format == MXQ_KV_MXFP8, tokens,
+                                     seqs->seqs, seqs->max_pages, cache->page_size, max_q);
 }
 
 MXQ_API mxq_status_t mxq_paged_attn(const uint16_t* q, uint16_t* out, float* lse, const mxq_kv_cache_t* cache,

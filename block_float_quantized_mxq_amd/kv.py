@@ -247,6 +247,7 @@ def rope(x, positions, inv_freq, layout="half", mscale=1.0, out=None, out_dtype=
     pos = _flat(positions, _I32, "positions", index, (n,))
     r = _rope_params(inv_freq, layout, mscale, index)
     if out is not None:
+        _first(out, _X, "out")
         out_dtype = out.dtype
     if out_dtype not in _X:
         raise TypeError(f"out must be float32 or bfloat16, got {out_dtype}")

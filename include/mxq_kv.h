@@ -126,7 +126,8 @@ mxq_status_t mxq_rope(const void *x, mxq_out_t x_dtype, void *y, mxq_out_t y_dty
  * the way, and rotates the queries: one launch between the QKV projection and
  * the attention.  A rotated key (and a value as it is) goes from fp32 to the
  * cache's format in one rounding: to bf16, or per 32 elements by the MX
- * conversion of mxq_quantize.
+ * conversion of mxq_quantize; 32 elements with an infinity or a NaN among them
+ * get the scale byte 255, which reads as NaN.
  *   k, v       fp32 or bf16 (x_dtype) [tokens][kv_heads][head_dim], k_stride
  *              and v_stride elements apart
  *   q, q_out   both or neither: queries [tokens][heads][head_dim] (q_stride)
@@ -137,7 +138,8 @@ mxq_status_t mxq_rope(const void *x, mxq_out_t x_dtype, void *y, mxq_out_t y_dty
  *   head_dim   64, 128 or 256;  page_size a power of two, 16 ..
  *              MXQ_KV_MAX_PAGE;  seqs up to MXQ_KV_MAX_SEQS;  tokens up to
  *              2^22;  heads up to 65536;  tokens * heads up to 2^25, seqs *
- *              kv_heads up to 2^22;  strides up to 2^36;  max_pages * page_size up to 2^30;  strides and pointers as in mxq_rope
+ *              kv_heads up to 2^22;  max_pages * page_size up to 2^30;
+ *              strides up to 2^36, otherwise as in mxq_rope, as the pointers
  * A token whose p is negative or beyond the table, or whose page is outside
  * [0, num_pages), stores nothing in the cache (its query is still rotated).
  * Two sequences that append to one page must not do so at the same row.

@@ -215,3 +215,35 @@ def test_log_sum_exp_joins_two_caches():
     assert ((joined - whole).abs() <= bound).all()
     total = torch.logsumexp(torch.stack([p[1] for p in parts]), 0)
     assert ((total - whole_lse.double()).abs() <= 2.0 ** -18 * (1 + total.abs())).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("seqs,heads,kv_heads,dim,window", [
+    ([(1300, 1500), (3, 400), (40, 90)], 8, 1, 256, 0), ([(900, 900), (700, 2000)], 4, 2, 256, 333),
+    ([(210, 700)], 20, 4, 256, 0), ([(1300, 1500), (3, 400), (40, 90)], 6, 2, 64, 0), ([(1800, 1800)], 16, 16, 64, 257)])
+def test_long_prompts_of_other_heads(seqs, heads, kv_heads, dim, window, fmt):
+    """Heads of 256 (two waves share their rows) and of 64, whole and in shares, with sequences of few rows among them."""
+    _check(Case(seqs, heads, kv_heads, dim, fmt, 32, seed=dim + window), f"prompt {dim} {seqs} {fmt}", window)
+
+
+def test_wide_heads_with_values_that_are_not_finite_and_missing_pages():
+    """As for heads of 128: in either half of the elements, and in a prompt that is split."""
+    for seqs, heads in (([(700, 820)], 8), ([(60, 2000), (2, 300)], 4)):
+        c = Case(seqs, heads, 2, 256, "bf16", 16, seed=70)
+        total = seqs[0][1]
+        for p, h, e in ((total - 1, 1, 200), (total - 30, 0, 5), (total - 55, 1, 131)):
+            c.half["v"][0][int(c.table[0, p // 16]), h, p % 16, e] = float("nan")
+        _check(c, f"values {seqs}")
+        p = total - 40
+        c.half["k"][0][int(c.table[0, p // 16]), 1, p % 16, 250] = float("nan")
+        _check(c, f"keys {seqs}")
+        c.table[0, (total - 20) // 16] = c.pages
+        _check(c, f"pages {seqs}")
+
+
+def test_rope_refuses_an_output_that_is_no_tensor():
+    x = torch.zeros(2, 2, 64, device=DEV)
+    pos, inv = torch.zeros(2, dtype=torch.int32, device=DEV), mxq.rope_inv_freq(64)[0]
+    for out in ([1], torch.zeros(2, 2, 64), torch.zeros(2, 2, 64, dtype=torch.float16, device=DEV)):
+        with pytest.raises(TypeError):
+            mxq.rope(x, pos, inv, out=out)

@@ -214,3 +214,13 @@ def test_inverse_frequency_refusals():
     assert call(rot=0) == SHAPE and call(rot=7) == SHAPE and call(theta=1.0) == SHAPE and call(theta=math.nan) == SHAPE
     assert call(sc=1, factor=0.5) == SHAPE and call(sc=3, context=0.0) == SHAPE and call(sc=3, low=32.0) == SHAPE
     assert call(sc=4, low=0.0) == SHAPE and call(sc=3, high=math.inf) == SHAPE and call(rot=1026) == UNSUPPORTED
+
+
+def test_sizes_whose_products_pass_64_bits():
+    """Refused by their own limit, whatever a product of them would wrap to."""
+    assert append(seqs=1 << 62, hk=4, heads=4, kstr=256, vstr=256) == UNSUPPORTED
+    assert attn(seqs=1 << 62, hk=4) == UNSUPPORTED
+    assert rope(xs=1 << 62) == UNSUPPORTED and append(qs=1 << 62) == UNSUPPORTED and attn(qs=1 << 62) == UNSUPPORTED
+    assert rope(xs=(1 << 62) + 1) == ALIGN
+    assert rope(heads=1 << 62) == SHAPE and append(heads=1 << 62, hk=1 << 62) == SHAPE
+    assert append(width=1 << 62, stride=1 << 62) == UNSUPPORTED and append(page=1 << 62) == UNSUPPORTED
