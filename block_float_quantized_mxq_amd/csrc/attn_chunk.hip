@@ -327,7 +327,6 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_chunk_kernel(AttnArgs a, Attn
                     l += p0 + p1;
                     p[2 * b + i / 8][(i / 2) % 4] = pack_bf16(p0, p1);
                 }
-            if (more) store_k(number + 1);
             // ---- values ----
             const uint8_t* vt = v_lds[number & 1];
             const int kq = (lane & 15) / 4;  // row of this lane in a transpose read
@@ -345,7 +344,10 @@ __global__ __launch_bounds__(64 * NW, 2) void attn_chunk_kernel(AttnArgs a, Attn
                     o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v),
                                                                    __builtin_bit_cast(bf16x8, p[t]), o[d], 0, 0, 0);
                 }
-            if (more) store_v(k0 + kKeys, number + 1, bad_next);
+            if (more) {
+                store_k(number + 1);
+                store_v(k0 + kKeys, number + 1, bad_next);
+            }
             bad = bad_next;
             __syncthreads();
         }
