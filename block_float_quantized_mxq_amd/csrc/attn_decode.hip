@@ -86,9 +86,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void attn_dec
     }
 
     f32x4 o[DB];
-#pragma unroll
-    for (int d = 0; d < DB; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    float m = -__builtin_inff(), l = 0.0f;
+    float m, l;
 
     const int ps = a.cache.page_shift, pmask = (1 << ps) - 1;
     const int32_t* table = a.seqs.table + sid * a.seqs.table_stride;
@@ -131,11 +129,20 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void attn_dec
     // 32 bytes that 32 lanes read by columns hit distinct banks.
     uint8_t* vt = lds + wave * kValueBytes;
     auto swizzle = [&](int row) __attribute__((always_inline)) { return D == 64 ? ((row >> 1) & 3) << 1 : (row & 7) << 1; };
-    bool taken_out = false;
-
     const int step = 4 * kBlock;
-    int k0 = begin + wave * kBlock;
-    if (k0 < end) {
+    // Both parts of a weight times an infinite value may make NaN of it.  If a
+    // sum comes out as NaN, the wave takes its blocks once more with all values
+    // that are not finite out of the products, as those always are that only
+    // some rows see.
+    bool taken_out = false, all_out = false;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d) o[d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        m = -__builtin_inff();
+        l = 0.0f;
+        int k0 = begin + wave * kBlock;
+        if (k0 >= end) break;
         int p0 = page_of(k0), p1 = page_of(k0 + 16);
         load_k(k0, p0, p1);
         load_v(k0, p0, p1);
@@ -144,6 +151,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void attn_dec
             const bool more = k0 + step < end;
             const bool bad0 = !in_range(p0), bad1 = k0 + 16 < end && !in_range(p1);
             const bool edge = k0 + kBlock > hi_in || k0 < lo_in || k0 + kBlock > end || bad0 || bad1;
+            const bool out = all_out || (edge && mixed);  // values that are not finite
             // ---- scores ----
             f32x4 s[2];
 #pragma unroll
@@ -175,12 +183,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void attn_dec
                 } else {
                     w[0] = vx[n];
                 }
-                if (edge) {
+                if (edge || all_out) {
                     const bool keep = (k0 + row < end) & (k0 + row >= lo_out) & !(row < 16 ? bad0 : bad1);
 #pragma unroll
                     for (int i = 0; i < W; ++i) {
                         if (!keep) w[i] = u32x4_t{0, 0, 0, 0};
-                        if (mixed) taken_out |= take_out_not_finite(w[i]);
+                        if (out) taken_out |= take_out_not_finite(w[i]);
                     }
                 }
 #pragma unroll
@@ -239,19 +247,26 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : D == 128 ? 3 : 4) void attn_dec
                 o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8, pl), o[d], 0, 0, 0);
             }
         }
-        if (__any(taken_out)) {
-            // values that are not finite, staged as zeros: added where a row sees them
-#pragma unroll 1
-            for (int b = begin + wave * kBlock; b < end; b += step) {
-#pragma unroll 1
-                for (int key = b; key < b + kBlock && key < end; ++key) {
-                    const int page = page_of(key);
-                    if (!in_range(page) || !(b + kBlock > hi_in || b < lo_in)) continue;
-                    const int64_t row = (((int64_t)page * a.cache.heads + kvh) << ps) + (key & pmask);
+        bool none = true;
 #pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        o[d] += not_finite_part<FMT>(a.cache.v, a.cache.vs, row, D, 16 * d + 4 * quad, (key >= lo) & (key < hi));
-                }
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) none &= o[d][i] == o[d][i];
+        if (all_out || __all(none)) break;
+        all_out = true;
+    }
+    if (__any(taken_out)) {
+        // values that are not finite, staged as zeros: added where a row sees them
+#pragma unroll 1
+        for (int b = begin + wave * kBlock; b < end; b += step) {
+#pragma unroll 1
+            for (int key = b; key < b + kBlock && key < end; ++key) {
+                const int page = page_of(key);
+                if (!in_range(page) || !(all_out || b + kBlock > hi_in || b < lo_in)) continue;
+                const int64_t row = (((int64_t)page * a.cache.heads + kvh) << ps) + (key & pmask);
+#pragma unroll
+                for (int d = 0; d < DB; ++d)
+                    o[d] += not_finite_part<FMT>(a.cache.v, a.cache.vs, row, D, 16 * d + 4 * quad, (key >= lo) & (key < hi));
             }
         }
     }

@@ -224,18 +224,28 @@ void choose_chunk(Choice* c, int64_t rows_head, int64_t kv_heads, int64_t dim, b
 // is a hint: if it puts every sequence's rows below kFewRows the decode kernel
 // takes all; else the chunk kernel runs, and beside it the decode kernel if the
 // number of tokens leaves room for sequences with few.
+//
+// The decode kernel also takes a call with more rows that has few tiles of 16
+// of them: it reads the keys once a tile, but from the caches, and spreads over
+// the device where the chunk kernel's tiles of 128 rows would be mostly empty
+// (one sequence, 32/4 heads of 128: 64 rows over 3000 positions 14 us against
+// 22, over 30000 40 and 51; 96 rows, 24 tiles, over 30000 68 and 52; 8/1 heads
+// of 256, 512 rows, 32 tiles, over 8000 35 and 47, over 30000 91 and 81; 8
+// sequences of 2000, 32/4 heads: 48 rows, 96 tiles, 31 and 26).
 Choice choose(int64_t group, int64_t kv_heads, int64_t dim, bool mx, int64_t tokens, int64_t seqs, int64_t positions,
               int64_t max_q) {
     const int64_t most_q = max_q < tokens ? max_q : tokens;
     Choice c{};
-    c.many = most_q * group > kFewRows;
+    const int64_t by_hint = (most_q * group + kFewRows - 1) / kFewRows * seqs, by_rows = tokens * group / kFewRows + seqs;
+    const int64_t tiles = (by_hint < by_rows ? by_hint : by_rows) * kv_heads;
+    c.many = most_q * group > kFewRows && tiles > (positions <= 8192 ? 32 : 16);
     c.few = !c.many || (seqs > 1 && 4 * tokens < 3 * seqs * most_q);
     if (c.few) {
         // Few tiles: about as many shares as workgroups are resident less one
         // a compute unit; more tiles have other lengths each, and more and
         // shorter shares even out the last round.  (Heads of 128: one token
         // over 131071 51 us in 512 shares, 64 in 2304.)
-        const int64_t units = (c.many ? seqs : tokens * group / kFewRows + seqs) * kv_heads;
+        const int64_t units = c.many ? seqs * kv_heads : tiles;
         c.target = units > 64 ? 9 * kDesignCus : (dim == 64 ? 3 : dim == 128 ? 2 : 1) * kDesignCus;
         // Short tables: the join's launch costs more than the split saves, in a
         // captured graph below 500 positions of heads of 128, called one by one

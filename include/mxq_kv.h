@@ -178,7 +178,9 @@ mxq_status_t mxq_kv_append(const void *q, const void *k, const void *v, mxq_out_
  * zeros and lse -inf.  kv_lens is taken as at most max_pages * page_size.  A
  * row that sees a position whose page is outside [0, num_pages) gets NaN.
  * What lies in cache rows that a token does not see, NaN and infinities
- * included, does not reach its output.
+ * included, does not reach its output.  An infinite value that it sees makes
+ * that element infinite (NaN where the other sign's meets it, or where its
+ * weight is below 2^-126).
  */
 mxq_status_t mxq_paged_attn(const uint16_t *q, uint16_t *out, float *lse, const mxq_kv_cache_t *cache,
                             const mxq_kv_seqs_t *seqs, int64_t tokens, int64_t heads, int64_t q_stride, float scale,

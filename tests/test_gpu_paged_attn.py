@@ -292,3 +292,54 @@ def test_offsets_past_4_gib():
         w = torch.softmax(a, -1)
         ref, mag = (w @ vv).transpose(0, 1), (w @ vv.abs()).transpose(0, 1)
         assert ((out.double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -6.9 * mag).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("heads,kv_heads,dim,page", [(24, 24, 64, 16), (48, 24, 128, 32), (24, 24, 256, 16)])
+def test_tiles_of_many_rows(heads, kv_heads, dim, page, fmt):
+    """Many heads, so that even short chunks go to tiles of 128 rows: odd lengths, a window, empty rows, sequences
+    of few rows beside them."""
+    for seqs, window in (([(17, 17), (33, 64), (64, 65), (1, 77)], 0), ([(40, 25), (20, 0), (18, 18), (0, 0)], 0),
+                         ([(50, 150), (2, 90)], 37)):
+        _check(Case(seqs, heads, kv_heads, dim, fmt, page, seed=dim + window, front=1, behind=1),
+               f"many rows {seqs} {window}", window)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_tiles_of_many_rows_with_missing_pages_and_values_that_are_not_finite(dim):
+    c = Case([(80, 100), (30, 40)], 24, 24, dim, "bf16", 16, seed=dim)
+    for p, h, e in ((75, 1, dim - 2), (90, 23, 3), (99, 7, 40)):
+        c.half["v"][0][int(c.table[0, p // 16]), h, p % 16, e] = float("nan")
+    c.half["k"][0][int(c.table[1, 1]), 5, 9, 17] = float("nan")
+    _check(c, f"not finite {dim}")
+    for bad in (-1, c.pages, 2 ** 31 - 1, -2 ** 31):
+        c.table[0, 3] = bad  # positions 48 .. 63
+        _check(c, f"page {bad} {dim}")
+    c = Case([(60, 110), (1, 40)], 48, 24, dim, "mxfp8", 16, seed=dim + 1)
+    c.half["v"][1][int(c.table[0, 80 // 16]), 3, 80 % 16] = 255
+    c.half["k"][1][int(c.table[0, 95 // 16]), 9, 95 % 16, 0] = 255
+    _check(c, f"not finite mxfp8 {dim}")
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("heads,kv_heads,dim", [(8, 1, 64), (8, 1, 128), (16, 2, 256)])
+def test_few_tiles_of_few_rows(heads, kv_heads, dim, fmt):
+    """Up to 32 tiles of 16 rows: the same result whichever kernel takes them, and just beyond."""
+    for seqs in ([(3, 700)], [(13, 1900)], [(32, 400)], [(64, 90), (1, 9)], [(70, 1030)]):
+        _check(Case(seqs, heads, kv_heads, dim, fmt, 64, seed=len(seqs) + dim), f"few tiles {seqs}")
+
+
+@pytest.mark.parametrize("fmt_dim", [64, 128, 256])
+@pytest.mark.parametrize("new,heads,kv_heads", [(1, 8, 2), (30, 4, 1), (40, 24, 24)])
+def test_an_infinite_value_makes_its_element_infinite(new, heads, kv_heads, fmt_dim):
+    """Wherever it lies: among keys that every row sees (a weight as two bf16 would make NaN of it), in another share,
+    at the end."""
+    c = Case([(new, 1500)], heads, kv_heads, fmt_dim, "bf16", 16, seed=new)
+    for p, e, sign in ((5, 3, 1), (700, 9, -1), (1200, 20, 1), (1500 - new, 31, -1), (1499, 40, 1)):
+        c.half["v"][0][int(c.table[0, p // 16]), 0, p % 16, e] = sign * math.inf
+    scale = c.dim ** -0.5
+    out = mxq.paged_attn(c.q16.to(DEV), c.cache(), *c.meta(), scale=scale, max_q=new).cpu().double()
+    ref, mag = c.attention(scale)[:2]
+    fine = ref.isfinite()
+    assert (~fine).sum() >= 4 * new and torch.equal(out[~fine], ref[~fine]) and torch.equal(out.isfinite(), fine)
+    assert ((out - ref).abs()[fine] <= 2.0 ** -6 * mag[fine]).all()
