@@ -203,10 +203,10 @@ MXQ_API mxq_status_t mxq_paged_attn(const uint16_t* q, uint16_t* out, float* lse
     const int64_t need = mxq_paged_attn_workspace(cache, seqs, tokens, heads, max_q);
     if (need > 0 && !workspace) return MXQ_E_NULLPTR;
     if (workspace_bytes < need) return MXQ_E_SHAPE;
-    int cus = 0;
+    int cus = 0;  // not used: the split is sized for 256, so that the workspace's size does not depend on the device
     mxq_status_t st;
     if ((st = mxq::check_device(&cus)) != MXQ_OK) return st;
     const mxq::AttnArgs a{q, out, lse, cache_of(*cache), seqs_of(*seqs), tokens, heads, q_stride, scale, (int)window,
-                          max_q, workspace, cus};
+                          max_q, workspace};
     return mxq::launched(mxq::launch_paged_attn(a, mxq::as_stream(stream)));
 }

@@ -27,10 +27,12 @@
 // of a wave that shares its SIMD: two waves share 32 rows, both take the whole
 // first product and each half of the output's elements.  That is half as much
 // matrix work again, and still faster than one wave a SIMD (a prompt of 4096
-// tokens, 16/2 heads: 229 us against 290).
+// tokens, 16/2 heads, in 3 shares: 331 us against 400; in one 229).
 //
-// Measured (MI355X; bf16, 40/8 heads of 128): a prompt of 8192 tokens 705 us,
-// 975 TFLOP/s; 512 tokens over 16000 192 us with the join, 890 TFLOP/s.  A
+// Measured (MI355X; bf16, 40/8 heads of 128): a prompt of 8192 tokens 710 us,
+// 970 TFLOP/s; 512 tokens over 16000 191 us with the join, 890 TFLOP/s; 2
+// prompts of 4000, window 1024, 32/8 heads of 64, 107 us, 610 TFLOP/s, where a
+// score has half the matrix work and the same vector work.  A
 // library matrix product of 8192 x 8192 x 8192 takes 1390-1480 TFLOP/s, and a
 // loop of nothing but these MFMAs on such data 1756: the power limit, not the
 // issue rate, ends both.  Here the softmax's vector work and the staging share

@@ -16,8 +16,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// Rows of one sequence and key/value head up to which the decode kernel takes
-// it; above, the chunk kernel does.
+// Rows of a tile of the decode kernel.  Where both kernels run, it takes the
+// sequences of one such tile per key/value head, and the chunk kernel the others.
 constexpr int kFewRows = 16;
 // Key tiles are split in multiples of this many positions.
 constexpr int kSplitUnit = 64;
@@ -305,6 +305,5 @@ inline int64_t decode_shares(const AttnArgs& a, const AttnPlan& p) {
 
 bool launch_attn_chunk(const AttnArgs& a, const AttnPlan& p, hipStream_t st);
 bool launch_attn_decode(const AttnArgs& a, const AttnPlan& p, hipStream_t st);
-
 
 }  // namespace mxq

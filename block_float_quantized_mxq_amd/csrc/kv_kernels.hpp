@@ -74,7 +74,6 @@ struct AttnArgs {
     int window;  // 0: none
     int64_t max_q;
     void* workspace;
-    int cus;
 };
 
 bool launch_rope(const RopeArgs& a, hipStream_t st);
