@@ -247,3 +247,97 @@ def test_rope_refuses_an_output_that_is_no_tensor():
     for out in ([1], torch.zeros(2, 2, 64), torch.zeros(2, 2, 64, dtype=torch.float16, device=DEV)):
         with pytest.raises(TypeError):
             mxq.rope(x, pos, inv, out=out)
+
+
+@pytest.mark.parametrize("seqs,heads,kv_heads", [([(1, 300), (2, 90)], 8, 2), ([(60, 200), (1, 90)], 24, 24)])
+def test_queries_that_are_slices_of_a_row(seqs, heads, kv_heads):
+    """The same bits as from contiguous queries: bf16 slices of a fused row, as a model without rotation has them."""
+    c = Case(seqs, heads, kv_heads, 128, "bf16", 16, seed=91)
+    q, args = c.q16.to(DEV), (c.cache(), *c.meta())
+    row = torch.full((c.tokens, (heads + 2 * kv_heads) * 128 + 8), 9.0, dtype=torch.bfloat16, device=DEV)
+    part = row[:, 8:8 + heads * 128].unflatten(1, (heads, 128))
+    part.copy_(q)
+    assert not part.is_contiguous()
+    assert torch.equal(mxq.paged_attn(part, *args, max_q=c.max_q), mxq.paged_attn(q, *args, max_q=c.max_q))
+
+
+@pytest.mark.parametrize("seqs,heads,kv_heads,dim", [
+    ([(200, 900), (1, 700), (2, 60)], 24, 8, 128), ([(40, 3000)], 64, 8, 256), ([(3, 800), (1, 90)], 8, 1, 64)])
+def test_captured_chunks(seqs, heads, kv_heads, dim):
+    """Chunks beside decode, chunks in shares, and few tiles, captured: replays follow the lengths and the tables."""
+    c = Case(seqs, heads, kv_heads, dim, "bf16", 16, seed=92)
+    q, cache, (table, cu, lens) = c.q16.to(DEV), c.cache(), c.meta()
+    for t in (cache.k, cache.v):
+        t.nan_to_num_(nan=0.5)  # rows of no sequence become visible below
+    out, lse = torch.empty_like(q), torch.empty(c.tokens, heads, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mxq.paged_attn(q, cache, table, cu, lens, max_q=c.max_q, out=out, lse=lse)
+    for _ in range(4):
+        out.zero_()
+        lse.zero_()
+        graph.replay()
+        want_lse = torch.empty_like(lse)
+        want = mxq.paged_attn(q, cache, table, cu, lens, max_q=c.max_q, lse=want_lse)
+        torch.cuda.synchronize()
+        # bits: a rolled table has pages that do not exist, and NaN in the rows that see them
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+        assert torch.equal(lse.view(torch.int32), want_lse.view(torch.int32))
+        lens.sub_(17)
+        table.copy_(table.roll(1, 1))
+
+
+def test_captured_rope():
+    x = torch.randn(9, 4, 128, device=DEV)
+    pos = torch.arange(9, dtype=torch.int32, device=DEV)
+    inv, _ = mxq.rope_inv_freq(128)
+    out = torch.empty(9, 4, 128, dtype=torch.bfloat16, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mxq.rope(x, pos, inv, out=out)
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, mxq.rope(x, pos, inv))
+        pos += 1000
+        x.normal_()
+
+
+@pytest.mark.parametrize("new", [1, 3])
+def test_the_most_sequences(new):
+    """4096 sequences: one key each that is theirs alone, all others share a page."""
+    n, h, hk, d = 4096, 8, 2, 64
+    g = torch.Generator(device=DEV).manual_seed(93)
+    k, v = (torch.randn(n + 1, hk, 16, d, device=DEV, generator=g).bfloat16() for _ in range(2))
+    table = torch.stack([torch.full((n,), n, device=DEV), torch.arange(n, device=DEV)], 1).int()
+    cu = torch.arange(n + 1, dtype=torch.int32, device=DEV) * new
+    lens = torch.full((n,), 16 + new, dtype=torch.int32, device=DEV)
+    q = torch.randn(n * new, h, d, device=DEV, generator=g).bfloat16()
+    out = mxq.paged_attn(q, mxq.KVCache(k, v), table, cu, lens, scale=0.125, max_q=new).double()
+    for t in (0, new - 1, 5 * new, 4095 * new, n * new - 1, 2048 * new + new - 1):
+        s, i = t // new, t % new
+        keys, vals = (torch.cat([x[n], x[s, :, :i + 1]], 1).double() for x in (k, v))
+        for head in range(h):
+            p = torch.softmax(0.125 * (keys[head // 4] @ q[t, head].double()), 0)
+            ref, mag = p @ vals[head // 4], p @ vals[head // 4].abs()
+            assert ((out[t, head] - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -12 * mag).all(), (t, head)
+
+
+def test_a_prompt_of_many_tokens():
+    """20000 tokens, sampled: the first, the last, and around the edges of tiles."""
+    n, h, hk, d, page = 20000, 16, 2, 128, 64
+    g = torch.Generator(device=DEV).manual_seed(94)
+    pages = -(-n // page)
+    k, v = (torch.randn(pages, hk, page, d, device=DEV, generator=g).bfloat16() for _ in range(2))
+    table = torch.randperm(pages, device=DEV, generator=g).int()[None]
+    cu, lens = (torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([0, n], [n]))
+    q = torch.randn(n, h, d, device=DEV, generator=g).bfloat16()
+    out = mxq.paged_attn(q, mxq.KVCache(k, v), table, cu, lens)
+    flat = [x[table[0].long()].transpose(0, 1).reshape(hk, -1, d) for x in (k, v)]
+    for t in (0, 1, 15, 16, 63, 64, 4095, 9999, 19967, 19968, 19999):
+        for head in (0, 7, 8, 15):
+            keys, vals = (x[head // 8, :t + 1].double() for x in flat)
+            p = torch.softmax(keys @ q[t, head].double() * d ** -0.5, 0)
+            ref, mag = p @ vals, p @ vals.abs()
+            # half a step of the output, and of each weight in numerator only: 2 * 2^-8 of sum p |v| covers both
+            assert ((out[t, head].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -7 * mag).all(), (t, head)
