@@ -27,7 +27,8 @@
 // of a wave that shares its SIMD: two waves share 32 rows, both take the whole
 // first product and each half of the output's elements.  That is half as much
 // matrix work again, and still faster than one wave a SIMD (a prompt of 4096
-// tokens, 16/2 heads, in 3 shares: 331 us against 400; in one 229).
+// tokens, 16/2 heads, in 3 shares: 331 us against 400; in one 229).  A
+// workgroup there has 64 or 128 rows.
 //
 // Measured (MI355X; bf16, 40/8 heads of 128): a prompt of 8192 tokens 710 us,
 // 970 TFLOP/s; 512 tokens over 16000 191 us with the join, 890 TFLOP/s; 2
@@ -80,7 +81,7 @@ struct Stage {
 };
 
 template <int D, int FMT, int NW>
-__global__ __launch_bounds__(64 * NW, 2) void attn_chunk_kernel(AttnArgs a, AttnPlan plan) {
+__global__ __launch_bounds__(64 * NW, D == 256 && NW == 4 ? 1 : 2) void attn_chunk_kernel(AttnArgs a, AttnPlan plan) {
     using T = Tile<D>;
     using St = Stage<D, FMT, NW>;
     constexpr int PARTS = kParts<D>, ROWS = 32 * NW / PARTS;
@@ -424,7 +425,10 @@ bool launch_attn_chunk(const AttnArgs& a, const AttnPlan& p, hipStream_t st) {
             if (p.waves == 8) launch_dim<128, 8>(a, p, st);
             else launch_dim<128, 4>(a, p, st);
             return true;
-        case 256: launch_dim<256, 8>(a, p, st); return true;
+        case 256:
+            if (p.waves == 8) launch_dim<256, 8>(a, p, st);
+            else launch_dim<256, 4>(a, p, st);
+            return true;
     }
     return false;
 }

@@ -181,20 +181,23 @@ struct Choice {
 // over 16k, 40/8 heads: 4 waves x 3 shares 220 us, 8 waves x 3 shares 195,
 // unsplit 420; a 1000-token prompt: 4 waves unsplit 37 us, 8 waves 41, 2 shares
 // 50.)  MXFP8 tiles take a sixth more.  Heads of 256 run one workgroup on a
-// compute unit, heads of 64 three.  Shares cost a launch and their partial sums
+// compute unit, of 8 waves and 128 rows (4.0 a tile) or, where those are few,
+// of 4 waves and 64 (3.4; a prompt of 545 tokens, 16/2 heads, 34 us against
+// 41), heads of 64 three.  Shares cost a launch and their partial sums
 // (a 4096-token prompt with 16/2 heads of 256: whole 229 us, 3 shares 326).
 //
 // most and mean: the tiles that the last row sees, and a row on average; rows
 // between see evenly fewer, so that some rows have nothing in the last shares.
 void choose_chunk(Choice* c, int64_t rows_head, int64_t kv_heads, int64_t dim, bool mx, double most, double mean) {
     const double more = mx ? 1.16 : 1.0;
-    const double full = (dim == 256 ? 4.0 : dim == 64 ? 1.9 : 2.3) * more;  // of all that are resident together
-    const double two = (dim == 256 ? 4.0 : dim == 64 ? 1.25 : 2.3) * more, alone = (dim == 256 ? 4.0 : dim == 64 ? 0.85 : 1.63) * more;
-    const double eight = 2.15 * more;
+    const double full = (dim == 256 ? 3.4 : dim == 64 ? 1.9 : 2.3) * more;  // of all that are resident together
+    const double two = (dim == 256 ? 3.4 : dim == 64 ? 1.25 : 2.3) * more, alone = (dim == 256 ? 3.4 : dim == 64 ? 0.85 : 1.63) * more;
+    const double eight = (dim == 256 ? 4.0 : 2.15) * more;
     const int64_t resident = (dim == 256 ? 1 : dim == 64 ? 3 : 2) * kDesignCus;
     double best = 1e30;
-    for (int waves = 4; waves <= (dim == 128 ? 8 : 4); waves += 4) {
-        const double units = (double)(((rows_head + 32 * waves - 1) / (32 * waves)) * kv_heads);
+    for (int waves = 4; waves <= (dim == 64 ? 4 : 8); waves += 4) {
+        const int64_t rows = (dim == 256 ? 16 : 32) * waves;
+        const double units = (double)(((rows_head + rows - 1) / rows) * kv_heads);
         const double slots = (double)(waves == 8 ? kDesignCus : resident), each = waves == 8 ? eight : full;
         for (int64_t s = 1; s <= kMaxSplits && (s == 1 || 64.0 * most >= 256.0 * (double)s); ++s) {
             // workgroups with something to do; their longest, mean and least work

@@ -341,3 +341,10 @@ def test_a_prompt_of_many_tokens():
             ref, mag = p @ vals, p @ vals.abs()
             # half a step of the output, and of each weight in numerator only: 2 * 2^-8 of sum p |v| covers both
             assert ((out[t, head].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -7 * mag).all(), (t, head)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("seqs,window", [([(2500, 2500)], 0), ([(1300, 1333), (1000, 2000)], 301), ([(2200, 2100)], 0)])
+def test_wide_heads_in_many_tiles(seqs, window, fmt):
+    """Heads of 256 in more tiles than compute units: workgroups of 128 rows and 8 waves."""
+    _check(Case(seqs, 16, 2, 256, fmt, 64, seed=95 + window), f"many tiles {seqs} {fmt}", window)
